@@ -101,7 +101,8 @@ def _quantise(x):
     """Codes (e4m3) and scales of rows x [..., d], in fp32."""
     x = x.float()
     a = x.abs().amax(-1).clamp(AMAX_LO, AMAX_HI)
-    return (x * (E4M3_MAX / a)[..., None]).to(torch.float8_e4m3fn), a / E4M3_MAX
+    up = torch.full_like(a, E4M3_MAX) / a           # a true division: number / tensor multiplies by a reciprocal
+    return (x * up[..., None]).to(torch.float8_e4m3fn), a / E4M3_MAX
 
 
 def _pages(shape, layout, make):
