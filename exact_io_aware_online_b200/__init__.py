@@ -15,7 +15,8 @@ import re
 
 __all__ = ["lib", "FAError", "FA_BF16", "FA_FP32", "fwd", "bwd", "bwd_workspace_size", "device_status",
            "exported_names", "set_timing_events", "bwd_noalloc", "fwd_splitkv", "fwd_blocksparse", "bwd_blocksparse", "fwd_varlen", "bwd_varlen", "fwd_strided", "bwd_strided",
-           "fwd_decode", "decode_splits", "fwd_packed", "bwd_packed", "debug_set_wait_limit", "debug_set_stall",
+           "fwd_decode", "decode_splits", "fwd_packed", "bwd_packed", "fwd_paged", "fwd_paged_workspace_size",
+           "cache_write", "cache_read", "debug_set_wait_limit", "debug_set_stall",
            "LIB_PATH", "HEADER_PATH"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +24,7 @@ LIB_PATH = os.path.join(HERE, "libfa.so")
 HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "fa.h")
 
 FA_BF16, FA_FP32 = 0, 1
+FA_CACHE_BF16, FA_CACHE_E4M3 = 0, 1
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_MISALIGNED",
           4: "FA_ERR_WORKSPACE", 5: "FA_ERR_CUDA", 6: "FA_ERR_TIMEOUT"}
 
@@ -93,6 +95,14 @@ def lib() -> ctypes.CDLL:
     L.fa_fwd_strided.restype = i
     L.fa_bwd_strided.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, f, i, i, vp, i, vp]
     L.fa_bwd_strided.restype = i
+    L.fa_cache_write.argtypes = [vp, vp, vp, vp, vp, i, i, vp]
+    L.fa_cache_write.restype = i
+    L.fa_cache_read.argtypes = [vp, vp, vp, vp, vp, i, i, vp]
+    L.fa_cache_read.restype = i
+    L.fa_fwd_paged.argtypes = [vp, vp, vp, vp, vp, i, i, f, i, i, vp, sz, i, vp]
+    L.fa_fwd_paged.restype = i
+    L.fa_fwd_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.fa_fwd_paged_workspace_size.restype = sz
     L.fa_debug_set_wait_limit.argtypes = [ctypes.c_ulonglong]
     L.fa_debug_set_wait_limit.restype = i
     L.fa_debug_set_stall.argtypes = [i]
@@ -566,6 +576,167 @@ def bwd_packed(q, k, v, o, lse, do, cu_seqlens, scale: float | None = None, caus
                _stream_ptr(q.device))
     _check(code, "fa_bwd_packed")
     return dq, dk, dv
+
+
+class _PagedCache(ctypes.Structure):
+    """fa_paged_cache of include/fa.h."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("seqlens", ctypes.c_void_p),
+                ("pages", _Strides), ("scales", _Strides), ("table_stride", ctypes.c_longlong),
+                ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
+    """Checks a paged cache's tensors against each other; the _PagedCache that
+    describes them (it holds pointers only: the tensors stay the caller's)."""
+    import torch
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages, v_pages must be 4-D [pages, kv heads, page size, head_dim]")
+    if k_pages.dtype == torch.bfloat16:
+        code = FA_CACHE_BF16
+    elif k_pages.dtype == torch.float8_e4m3fn:
+        code = FA_CACHE_E4M3
+    else:
+        raise TypeError(f"k_pages: unsupported dtype {k_pages.dtype} (bfloat16 or float8_e4m3fn)")
+    device, shape, st = k_pages.device, k_pages.shape, k_pages.stride()
+    if v_pages.shape != shape:
+        raise ValueError(f"v_pages: shape {tuple(v_pages.shape)}, expected {tuple(shape)}")
+    if v_pages.dtype != k_pages.dtype:
+        raise TypeError(f"v_pages: dtype {v_pages.dtype}, expected {k_pages.dtype}")
+    if v_pages.stride() != st or st[3] != 1:
+        raise ValueError("k_pages, v_pages must have the same strides and a contiguous last axis")
+    P, Hkv, page, d = shape
+    if page_table.dim() != 2 or seqlens.dim() != 1 or page_table.shape[0] != seqlens.shape[0]:
+        raise ValueError("page_table must be [sequences, pages of a sequence] and seqlens [sequences]")
+    if page_table.dtype != torch.int32 or seqlens.dtype != torch.int32:
+        raise TypeError("page_table and seqlens must be int32")
+    B, M = page_table.shape
+    if (M > 1 and page_table.stride(1) != 1) or (B > 1 and (page_table.stride(0) < M or seqlens.stride(0) != 1)):
+        raise ValueError("page_table must have contiguous rows that do not overlap, and seqlens must be contiguous")
+    if code == FA_CACHE_BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale, v_scale belong to a float8_e4m3fn cache")
+        scales = _Strides(0, 0, 0)
+        tensors = ((v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens"))
+    else:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None or t.shape != shape[:3] or t.dtype != torch.float32:
+                raise ValueError(f"{name}: must be a float32 tensor of shape {tuple(shape[:3])}")
+        if k_scale.stride() != v_scale.stride():
+            raise ValueError("k_scale, v_scale must have the same strides")
+        scales = _Strides(*k_scale.stride())
+        tensors = ((v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens"), (k_scale, "k_scale"),
+                   (v_scale, "v_scale"))
+    if not k_pages.is_cuda:
+        raise ValueError(f"k_pages: must be on a CUDA device, got {device}")
+    for t, name in tensors:
+        if t.device != device:
+            raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {device})")
+    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr() if code else None,
+                       v_scale.data_ptr() if code else None, page_table.data_ptr(), seqlens.data_ptr(),
+                       _Strides(st[0], st[1], st[2]), scales, page_table.stride(0), B, Hkv, d, P, page, M, code)
+
+
+def _move_args(c, k, v, cu_seqlens, T, device):
+    """Checks the packed tokens k, v [T, Hkv, d] (d contiguous) and the device
+    offsets of cache_write() / cache_read(); their fa_strides."""
+    import torch
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dim() != 3 or tuple(t.shape) != (T, c.Hkv, c.d):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, c.Hkv, c.d)}")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+        if t.stride(2) != 1:
+            raise ValueError(f"{name}: must have a contiguous last axis")
+        if t.device != device:
+            raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {device})")
+    if cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (c.B + 1,) or cu_seqlens.device != device \
+            or cu_seqlens.stride(0) != 1:
+        raise TypeError(f"cu_seqlens must be a contiguous int32 tensor of {c.B + 1} values on the device of k_pages")
+    return (_Strides * 2)(_Strides(1, k.stride(1), k.stride(0)), _Strides(1, v.stride(1), v.stride(0)))
+
+
+def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale=None, v_scale=None):
+    """Writes the packed tokens k, v [T,Hkv,d] (any token and head strides) into
+    a paged cache: rows cu_seqlens[b] .. cu_seqlens[b+1] are the newest of the
+    seqlens[b] tokens of sequence b (see fa_paged_cache and fa_cache_write in
+    fa.h).  k_pages, v_pages [P,Hkv,page,d], bfloat16 or, quantised with one
+    scale per token and kv head in k_scale, v_scale [P,Hkv,page] float32,
+    float8_e4m3fn; page_table [B,pages of a sequence], cu_seqlens and seqlens
+    int32, all on one CUDA device."""
+    c = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    T, device = k.shape[0], k_pages.device
+    st = _move_args(c, k, v, cu_seqlens, T, device)
+    if T == 0:
+        return
+    code = _on(device, lib().fa_cache_write, ctypes.addressof(c), k.data_ptr(), v.data_ptr(), ctypes.addressof(st),
+               cu_seqlens.data_ptr(), T, FA_BF16, _stream_ptr(device))
+    _check(code, "fa_cache_write")
+
+
+def cache_read(k_pages, v_pages, page_table, cu_seqlens, seqlens, num_tokens: int, k_scale=None, v_scale=None,
+               out=None):
+    """The inverse of cache_write(): k, v [num_tokens,Hkv,d] bfloat16, rows
+    cu_seqlens[b] .. cu_seqlens[b+1] the newest of sequence b's tokens (all of
+    them when the offsets are the lengths' running sum).  `out`=(k, v) may have
+    any token and head strides; its rows outside the offsets are left as they
+    were (uninitialised when allocated here)."""
+    import torch
+    c = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    T, device = int(num_tokens), k_pages.device
+    if out is None:
+        k = torch.empty((T, c.Hkv, c.d), dtype=torch.bfloat16, device=device)
+        v = torch.empty((T, c.Hkv, c.d), dtype=torch.bfloat16, device=device)
+    else:
+        k, v = out
+    st = _move_args(c, k, v, cu_seqlens, T, device)
+    if T == 0:
+        return k, v
+    code = _on(device, lib().fa_cache_read, ctypes.addressof(c), k.data_ptr(), v.data_ptr(), ctypes.addressof(st),
+               cu_seqlens.data_ptr(), T, FA_BF16, _stream_ptr(device))
+    _check(code, "fa_cache_read")
+    return k, v
+
+
+def fwd_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
+    return int(lib().fa_fwd_paged_workspace_size(B, H, Hkv, Nq, d))
+
+
+def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=None, scale: float | None = None,
+              causal: bool = False, window: int = -1, out=None, lse=None, workspace=None):
+    """O, LSE of each sequence's newest Nq tokens, q [B,H,Nq,d] (bfloat16, any
+    layout with d contiguous), over a paged cache that holds their keys and
+    values already: fwd_decode() for sequences of different lengths (see
+    fa_fwd_paged in fa.h; the cache's tensors are those of cache_write())."""
+    import torch
+    c = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    device = k_pages.device
+    if q.dim() != 4:
+        raise ValueError("q must be 4-D [batch, heads, rows, head_dim]")
+    B, H, Nq, d = q.shape
+    if B != c.B or d != c.d:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected {c.B} sequences of head_dim {c.d}")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q: dtype {q.dtype}, expected torch.bfloat16")
+    if q.device != device:
+        raise ValueError(f"q: must be on the CUDA device of k_pages, got {q.device} (k_pages: {device})")
+    if out is not None:
+        _same(out, q.shape, q, "out", contiguous=False)
+    if lse is not None:
+        _check_lse(lse, (B, H, Nq), q)
+    if workspace is not None:
+        _check_workspace(workspace, device)
+    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=device) if out is None else out
+    l = torch.empty((B, H, Nq), dtype=torch.float32, device=device) if lse is None else lse
+    st = _strides_of(q, o)
+    ws = torch.empty(max(fwd_paged_workspace_size(B, H, c.Hkv, Nq, d), 16), dtype=torch.uint8, device=device) \
+        if workspace is None else workspace
+    code = _on(device, lib().fa_fwd_paged, ctypes.addressof(c), q.data_ptr(), o.data_ptr(), l.data_ptr(),
+               ctypes.addressof(st), H, Nq, 1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
+               int(window), ws.data_ptr(), ws.numel(), FA_BF16, _stream_ptr(device))
+    _check(code, "fa_fwd_paged")
+    return o, l
 
 
 def set_timing_events(start=None, stop=None):

@@ -32,12 +32,12 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/fa_api.cu (which includes the kernels) into libfa.so."""
+    """Compile csrc/*.cu (which include the kernels) into libfa.so."""
     if not force and not stale():
         return LIB
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-o", tmp, os.path.join(CSRC, "fa_api.cu")]
+           "-t", "0", "-o", tmp, *sorted(glob.glob(os.path.join(CSRC, "*.cu")))]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     res = subprocess.run(cmd, capture_output=True, text=True)

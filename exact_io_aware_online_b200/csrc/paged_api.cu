@@ -1,0 +1,212 @@
+// paged_api.cu -- the paged-cache part of libfa.so's C ABI (include/fa.h):
+// argument checking and kernel launches.  A translation unit of its own, so
+// that the dense kernels' sources (which their captured profiles are keyed by)
+// do not depend on it.  Like there, every entry point validates on the host
+// first and enqueues nothing when an argument is bad.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <utility>
+
+#include "../../include/fa.h"
+#include "cache_sm100.cuh"
+#include "paged_sm100.cuh"
+
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The kernels run on the current device: a stream of another one is an
+// argument error (NULL is the current device's legacy stream).  A capturing
+// stream cannot be asked for its device without ending the capture; there the
+// launch itself fails on a foreign stream.
+fa_status check_stream(void* stream) {
+  int cur = 0, sdev = 0;
+  if (cudaGetDevice(&cur) != cudaSuccess) return FA_ERR_CUDA;
+  if (stream == nullptr) return FA_OK;
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capturing) != cudaSuccess) return FA_ERR_INVALID_ARG;
+  if (capturing != cudaStreamCaptureStatusNone) return FA_OK;
+  if (cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev) != cudaSuccess) return FA_ERR_INVALID_ARG;
+  return sdev == cur ? FA_OK : FA_ERR_INVALID_ARG;
+}
+
+template <typename... KArgs, typename... Args>
+fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Strides of an [n0, n1, n2, inner] tensor of esize-byte elements: positive,
+// below 2^40 bytes and multiples of `align` bytes; an axis of extent 1 is never
+// stepped, so its stride is replaced.  `output`: the layout must be one-to-one
+// (sorted by stride, each axis steps past the extent of the axes inside it).
+fa_status check_strides(const fa_strides& in, long long n0, long long n1, long long n2, int inner, int esize, int align,
+                        bool output, fa::Strides* out) {
+  struct Axis {
+    long long stride, extent;
+  } ax[3] = {{in.batch, n0}, {in.head, n1}, {in.row, n2}};
+  const long long lim = (1LL << 40) / esize;
+  for (Axis& a : ax) {
+    if (a.extent == 1) a.stride = 16;  // any aligned value
+    if (a.stride <= 0 || a.stride >= lim) return FA_ERR_INVALID_ARG;
+    if ((a.stride * esize) % align != 0) return FA_ERR_MISALIGNED;
+  }
+  *out = fa::Strides{ax[0].stride, ax[1].stride, ax[2].stride};
+  if (output) {
+    std::sort(ax, ax + 3, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+    long long span = inner;
+    for (const Axis& a : ax) {
+      if (a.extent == 1) continue;
+      if (a.stride < span) return FA_ERR_INVALID_ARG;
+      span = a.stride * a.extent;
+    }
+  }
+  return FA_OK;
+}
+
+// `written`: the pages are an output.
+fa_status check_cache(const fa_paged_cache* c, fa_dtype dtype, bool written, fa::CacheParams* p) {
+  if (!c || !c->k_pages || !c->v_pages || !c->page_table || !c->seqlens) return FA_ERR_INVALID_ARG;
+  if (c->B < 1 || c->Hkv < 1 || c->num_pages < 1 || c->page_size < 1 || c->max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+  if (c->dtype != FA_CACHE_BF16 && c->dtype != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+  if (c->B > 1 && c->table_stride < c->max_pages) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  // positions are 32-bit
+  if (static_cast<long long>(c->page_size) * c->max_pages > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  const bool quant = c->dtype == FA_CACHE_E4M3;
+  if (quant && (!c->k_scale || !c->v_scale)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return FA_ERR_MISALIGNED;
+  p->scales = fa::Strides{0, 0, 0};
+  fa_status s = check_strides(c->pages, c->num_pages, c->Hkv, c->page_size, c->d, quant ? 1 : 2, 16, written, &p->pages);
+  if (s != FA_OK) return s;
+  if (quant) {
+    if (((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) & 3u) != 0)
+      return FA_ERR_MISALIGNED;
+    s = check_strides(c->scales, c->num_pages, c->Hkv, c->page_size, 1, 4, 4, written, &p->scales);
+    if (s != FA_OK) return s;
+  }
+  p->k = static_cast<uint8_t*>(c->k_pages);
+  p->v = static_cast<uint8_t*>(c->v_pages);
+  p->ks = c->k_scale;
+  p->vs = c->v_scale;
+  p->table = c->page_table;
+  p->seqlens = c->seqlens;
+  p->table_stride = c->B > 1 ? c->table_stride : 0;
+  p->B = c->B;
+  p->Hkv = c->Hkv;
+  p->num_pages = c->num_pages;
+  p->page_size = c->page_size;
+  p->max_pages = c->max_pages;
+  return FA_OK;
+}
+
+template <bool kWrite>
+fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_strides* strides, const int* cu, int T,
+                      fa_dtype dtype, void* stream) {
+  fa::MoveParams p{};
+  fa_status s = check_cache(cache, dtype, kWrite, &p.c);
+  if (s != FA_OK) return s;
+  if (T < 0 || !cu) return FA_ERR_INVALID_ARG;
+  if (T == 0) return FA_OK;
+  if (!k || !v) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
+  const int d = cache->d, Hkv = cache->Hkv;
+  const fa_strides packed{1, d, static_cast<long long>(Hkv) * d};
+  fa::Strides sk, sv;
+  if ((s = check_strides(strides ? strides[0] : packed, 1, Hkv, T, d, 2, 16, !kWrite, &sk)) != FA_OK) return s;
+  if ((s = check_strides(strides ? strides[1] : packed, 1, Hkv, T, d, 2, 16, !kWrite, &sv)) != FA_OK) return s;
+  if ((s = check_stream(stream)) != FA_OK) return s;
+  p.k = static_cast<uint8_t*>(k);
+  p.v = static_cast<uint8_t*>(v);
+  p.k_row = sk.n;
+  p.k_head = sk.h;
+  p.v_row = sv.n;
+  p.v_head = sv.h;
+  p.cu = cu;
+  p.T = T;
+  const int rows = 256 / d * fa::kMoveUnroll;  // rows a warp moves
+  const long long tasks = static_cast<long long>(T) * ((2LL * Hkv + rows - 1) / rows);
+  const long long blocks = (tasks + fa::kMoveWarps - 1) / fa::kMoveWarps;
+  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(32 * fa::kMoveWarps);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool quant = cache->dtype == FA_CACHE_E4M3;
+  if (d == 64)
+    return quant ? launch(fa::cache_move_kernel<64, true, kWrite>, grid, block, 0, st, p)
+                 : launch(fa::cache_move_kernel<64, false, kWrite>, grid, block, 0, st, p);
+  return quant ? launch(fa::cache_move_kernel<128, true, kWrite>, grid, block, 0, st, p)
+               : launch(fa::cache_move_kernel<128, false, kWrite>, grid, block, 0, st, p);
+}
+
+bool paged_sizes_ok(int B, int H, int Hkv, int Nq) {
+  return B >= 1 && H >= 1 && Hkv >= 1 && Nq >= 1 && H % Hkv == 0 &&
+         static_cast<long long>(B) * H <= 0x7fffffffLL / Nq;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_cache_write(const fa_paged_cache* cache, const void* k, const void* v, const fa_strides* strides,
+                         const int* cu_seqlens_dev, int T, fa_dtype dtype, void* stream) {
+  return move_tokens<true>(cache, const_cast<void*>(k), const_cast<void*>(v), strides, cu_seqlens_dev, T, dtype,
+                           stream);
+}
+
+fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_strides* strides,
+                        const int* cu_seqlens_dev, int T, fa_dtype dtype, void* stream) {
+  return move_tokens<false>(cache, k, v, strides, cu_seqlens_dev, T, dtype, stream);
+}
+
+size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d) {
+  if (!paged_sizes_ok(B, H, Hkv, Nq) || (d != 64 && d != 128)) return 0;
+  return 256;
+}
+
+fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,
+                       int H, int Nq, float scale, int causal, int window, void* workspace, size_t ws_bytes,
+                       fa_dtype dtype, void* stream) {
+  if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale) || window < -1) return FA_ERR_INVALID_ARG;
+  fa::PagedParams p{};
+  fa_status s = check_cache(cache, dtype, false, &p.c);
+  if (s != FA_OK) return s;
+  const int B = cache->B, Hkv = cache->Hkv, d = cache->d;
+  if (!paged_sizes_ok(B, H, Hkv, Nq)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_MISALIGNED;
+  const fa_strides dense{static_cast<long long>(H) * Nq * d, static_cast<long long>(Nq) * d, d};
+  if ((s = check_strides(strides ? strides[0] : dense, B, H, Nq, d, 2, 16, false, &p.sq)) != FA_OK) return s;
+  if ((s = check_strides(strides ? strides[1] : dense, B, H, Nq, d, 2, 16, true, &p.so)) != FA_OK) return s;
+  if (!workspace || ws_bytes < fa_fwd_paged_workspace_size(B, H, Hkv, Nq, d)) return FA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FA_ERR_MISALIGNED;
+  if ((s = check_stream(stream)) != FA_OK) return s;
+  p.q = static_cast<const uint8_t*>(q);
+  p.o = static_cast<uint8_t*>(o);
+  p.lse = lse;
+  p.H = H;
+  p.Nq = Nq;
+  p.g = H / Hkv;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.causal = causal ? 1 : 0;
+  p.window = window < (1 << 30) ? window : -1;  // positions stay below 2^30
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long rows = static_cast<long long>(B) * H * Nq;
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  const bool quant = cache->dtype == FA_CACHE_E4M3;
+  if (d == 64)
+    return quant ? launch(fa::paged_row_kernel<64, true>, grid, 128, 0, st, p)
+                 : launch(fa::paged_row_kernel<64, false>, grid, 128, 0, st, p);
+  return quant ? launch(fa::paged_row_kernel<128, true>, grid, 128, 0, st, p)
+               : launch(fa::paged_row_kernel<128, false>, grid, 128, 0, st, p);
+}
+
+}  // extern "C"

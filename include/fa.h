@@ -238,6 +238,97 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
                         float scale, int causal, int window, fa_dtype dtype, void* stream);
 
 /*
+ * Paged key/value cache: the keys and values of B growing sequences, kept in
+ * pages of page_size tokens that belong to no sequence until the page table
+ * says so.  Position n of sequence b is token n % page_size of page
+ * page_table[b][n / page_size]; seqlens[b] is how many tokens sequence b holds.
+ *
+ *  pages    k_pages, v_pages [num_pages, Hkv, page_size, d], K and V at the
+ *           same element strides (`pages`: batch = page, head, row = token; d
+ *           contiguous), e.g. tokens inside heads or heads inside tokens.
+ *           Bases 16-byte aligned, strides positive multiples of 16 bytes.
+ *  dtype    FA_CACHE_BF16: bfloat16.  FA_CACHE_E4M3: 8-bit floats (4 exponent
+ *           and 3 mantissa bits, largest value 448) with one fp32 scale for
+ *           each token and kv head, k_scale, v_scale [num_pages, Hkv,
+ *           page_size] at the element strides `scales`; the value is code *
+ *           scale.  With a = max |x| over the row's d values, clamped to
+ *           [2^-100, FLT_MAX], scale = a / 448 and code = x * (448 / a), both
+ *           in fp32, the code rounded to nearest even.  A row that holds a NaN
+ *           has a NaN scale: it reads back as NaN throughout.  An infinite
+ *           value counts as FLT_MAX (which bf16 rounds to infinity again), next
+ *           to which ordinary values of its row become zero.
+ *  lengths  seqlens (device) is read by the kernels and clamped to [0,
+ *           max_pages * page_size].  page_table (device) holds B rows of
+ *           max_pages entries, table_stride entries apart.  Entries behind a
+ *           sequence's length are never read; an entry outside [0, num_pages)
+ *           stands for no page: its tokens are not written, read back as zero
+ *           and are not attended to.  Page table and lengths are read in stream
+ *           order, so they may change between the replays of a captured graph.
+ */
+typedef enum fa_cache_dtype { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_dtype;
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* k_scale; /* FA_CACHE_E4M3; ignored otherwise */
+  float* v_scale;
+  const int* page_table;
+  const int* seqlens;
+  fa_strides pages, scales;
+  long long table_stride;
+  int B, Hkv, d, num_pages, page_size, max_pages;
+  fa_cache_dtype dtype;
+} fa_paged_cache;
+
+/*
+ * Write tokens into the cache / read them back.  Tokens are packed along the
+ * first axis: k, v [T, Hkv, d] bf16 at the element strides strides[0] (k) and
+ * strides[1] (v) (row = token, head; `batch` is ignored; NULL: contiguous),
+ * e.g. slices of a fused projection's output.  cu_seqlens_dev: DEVICE pointer
+ * to B + 1 non-decreasing offsets; rows [cu[b], cu[b+1]) are the NEWEST tokens
+ * of sequence b: with n_b of them, row cu[b] + i is position seqlens[b] - n_b +
+ * i, so seqlens counts the tokens of this call.  Rows whose position is
+ * negative are not written, and read back as zero; rows outside [cu[0], cu[B])
+ * are not read, and left as they are.  Everything but these rows' places in the
+ * cache stays as it was.  Two rows of one call must not share a place (two
+ * sequences with the same page): which one it then holds is not defined.
+ * fa_cache_read writes k and v, whose layout must be one-to-one as for an output
+ * of fa_fwd_strided (and so must the pages' for fa_cache_write).
+ * T = 0 enqueues nothing.  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
+ * Errors: FA_ERR_INVALID_ARG for null pointers, sizes < 1, T < 0 or bad
+ * strides; FA_ERR_UNSUPPORTED for d not in {64, 128}; FA_ERR_MISALIGNED.
+ */
+fa_status fa_cache_write(const fa_paged_cache* cache, const void* k, const void* v, const fa_strides* strides,
+                         const int* cu_seqlens_dev, int T, fa_dtype dtype, void* stream);
+fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_strides* strides,
+                        const int* cu_seqlens_dev, int T, fa_dtype dtype, void* stream);
+
+/*
+ * Attention of each sequence's newest Nq tokens over the paged cache, forward
+ * only: fa_fwd_decode for sequences of different lengths.  q, o [B, H, Nq, d]
+ * bf16 at the element strides strides[0] (q) and strides[1] (o) (NULL:
+ * contiguous), lse [B, H, Nq] contiguous fp32.  Query row i of sequence b sits
+ * at position seqlens[b] - Nq + i, keys are the positions below seqlens[b], and
+ * the causal / window predicate applies to positions, as in fa_fwd_decode.  The
+ * tokens' own keys and values must be in the cache already (fa_cache_write
+ * first).  Rows with a negative position (sequences shorter than Nq), and rows
+ * without an allowed key, get O = 0, LSE = -inf; what masked tokens and unused
+ * parts of pages hold has no effect.  Every key and value that some row may see
+ * is read once for the H / Hkv query heads that share it, as long as their
+ * (H / Hkv) * Nq rows are at most 64 (once per 64 rows otherwise).
+ * The key ranges of all sequences are dealt out evenly over the SMs, and
+ * sequences that several of them share are merged from partial online-softmax
+ * states (fa_fwd_splitkv) in the workspace: at least
+ * fa_fwd_paged_workspace_size() bytes of device memory, 16-byte aligned,
+ * contents irrelevant on entry, not shared by calls that may overlap.
+ * Deterministic; a sequence's last bits depend on the other lengths of the
+ * batch.  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
+ */
+size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d);
+fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,
+                       int H, int Nq, float scale, int causal, int window, void* workspace, size_t ws_bytes,
+                       fa_dtype dtype, void* stream);
+
+/*
  * Bytes of device workspace fa_bwd needs for these sizes (fp32 row terms
  * D_i = sum_k dO_ik O_ik, prescaled LSE, and for bf16 a float dQ accumulator).
  * Returns 0 for sizes fa_bwd would reject.
