@@ -33,13 +33,20 @@ fa_status check_stream(void* stream) {
   return sdev == cur ? FA_OK : FA_ERR_INVALID_ARG;
 }
 
+// dependent: the kernel starts early and waits (griddepcontrol.wait) for the one before it.
 template <typename... KArgs, typename... Args>
-fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool dependent,
+                 Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -141,10 +148,40 @@ fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_st
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = cache->dtype == FA_CACHE_E4M3;
   if (d == 64)
-    return quant ? launch(fa::cache_move_kernel<64, true, kWrite>, grid, block, 0, st, p)
-                 : launch(fa::cache_move_kernel<64, false, kWrite>, grid, block, 0, st, p);
-  return quant ? launch(fa::cache_move_kernel<128, true, kWrite>, grid, block, 0, st, p)
-               : launch(fa::cache_move_kernel<128, false, kWrite>, grid, block, 0, st, p);
+    return quant ? launch(fa::cache_move_kernel<64, true, kWrite>, grid, block, 0, st, false, p)
+                 : launch(fa::cache_move_kernel<64, false, kWrite>, grid, block, 0, st, false, p);
+  return quant ? launch(fa::cache_move_kernel<128, true, kWrite>, grid, block, 0, st, false, p)
+               : launch(fa::cache_move_kernel<128, false, kWrite>, grid, block, 0, st, false, p);
+}
+
+// The workspace: split[CTAs] (int4), part_m[2 * CTAs][rows] (float4), part_o[2 * CTAs][rows][d] (float)
+struct PagedOffsets {
+  size_t part_m, part_o, bytes;
+};
+PagedOffsets paged_offsets(int rows, int d) {
+  PagedOffsets w;
+  w.part_m = fa::kPagedMaxCtas * sizeof(int4);
+  w.part_o = w.part_m + sizeof(float4) * 2 * fa::kPagedMaxCtas * rows;
+  w.bytes = w.part_o + sizeof(float) * 2 * fa::kPagedMaxCtas * rows * d;
+  return w;
+}
+
+template <int D, bool kQuant, int RB>
+fa_status launch_paged(const fa::PagedParams& p, int ctas, cudaStream_t st) {
+  constexpr int smem = fa::PagedCfg<D, kQuant, RB>::kSmemBytes;
+  const auto kernel = fa::paged_kernel<D, kQuant, RB>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
+  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), smem, st, false, p);
+  if (s != FA_OK) return s;
+  const dim3 grid(ctas, (p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
+  return launch(fa::paged_combine_kernel<D>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, 16 * RB);
+}
+
+template <int D, bool kQuant>
+fa_status launch_paged_rows(const fa::PagedParams& p, int ctas, cudaStream_t st) {
+  if (p.R <= 16) return launch_paged<D, kQuant, 1>(p, ctas, st);
+  if (p.R <= 32) return launch_paged<D, kQuant, 2>(p, ctas, st);
+  return launch_paged<D, kQuant, 4>(p, ctas, st);
 }
 
 bool paged_sizes_ok(int B, int H, int Hkv, int Nq) {
@@ -169,7 +206,8 @@ fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_
 
 size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d) {
   if (!paged_sizes_ok(B, H, Hkv, Nq) || (d != 64 && d != 128)) return 0;
-  return 256;
+  const long long R = static_cast<long long>(H / Hkv) * Nq;
+  return paged_offsets(static_cast<int>(std::min(R, 64LL)), d).bytes;
 }
 
 fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,
@@ -199,14 +237,23 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.causal = causal ? 1 : 0;
   p.window = window < (1 << 30) ? window : -1;  // positions stay below 2^30
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long rows = static_cast<long long>(B) * H * Nq;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  p.R = p.g * Nq;
+  const int block = p.R <= 16 ? 16 : p.R <= 32 ? 32 : 64;
+  p.nblk = (p.R + block - 1) / block;
+  p.prow = std::min(p.R, block);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const PagedOffsets at = paged_offsets(p.prow, d);
+  p.split = reinterpret_cast<int4*>(ws);
+  p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
+  p.part_o = reinterpret_cast<float*>(ws + at.part_o);
+  // no more CTAs than the lengths could give tiles
+  const long long cap = static_cast<long long>(cache->max_pages) * cache->page_size;
+  const double tiles = static_cast<double>((cap + fa::kPagedTile - 1) / fa::kPagedTile) * B * Hkv * p.nblk;
+  if (tiles / fa::kPagedMaxCtas > 1e9) return FA_ERR_UNSUPPORTED;  // a CTA counts its tiles in 32 bits
+  const int ctas = static_cast<int>(std::min<double>(fa::kPagedMaxCtas, tiles));
   const bool quant = cache->dtype == FA_CACHE_E4M3;
-  if (d == 64)
-    return quant ? launch(fa::paged_row_kernel<64, true>, grid, 128, 0, st, p)
-                 : launch(fa::paged_row_kernel<64, false>, grid, 128, 0, st, p);
-  return quant ? launch(fa::paged_row_kernel<128, true>, grid, 128, 0, st, p)
-               : launch(fa::paged_row_kernel<128, false>, grid, 128, 0, st, p);
+  if (d == 64) return quant ? launch_paged_rows<64, true>(p, ctas, st) : launch_paged_rows<64, false>(p, ctas, st);
+  return quant ? launch_paged_rows<128, true>(p, ctas, st) : launch_paged_rows<128, false>(p, ctas, st);
 }
 
 }  // extern "C"
