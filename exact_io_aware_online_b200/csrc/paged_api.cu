@@ -166,22 +166,30 @@ PagedOffsets paged_offsets(int rows, int d) {
   return w;
 }
 
-template <int D, bool kQuant, int RB>
-fa_status launch_paged(const fa::PagedParams& p, int ctas, cudaStream_t st) {
-  constexpr int smem = fa::PagedCfg<D, kQuant, RB>::kSmemBytes;
-  const auto kernel = fa::paged_kernel<D, kQuant, RB>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
-  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), smem, st, false, p);
+int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // rows of a unit
+
+template <int D, bool kQuant, int NB, int RG>
+fa_status launch_paged(const fa::PagedParams& p, double tiles, cudaStream_t st) {
+  using C = fa::PagedCfg<D, kQuant, NB, RG>;
+  const auto kernel = fa::paged_kernel<D, kQuant, NB, RG>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+    return FA_ERR_CUDA;
+  // no more CTAs than the lengths could give tiles
+  const int ctas = static_cast<int>(std::min<double>(148 * C::kCtas, tiles));
+  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, p);
   if (s != FA_OK) return s;
   const dim3 grid(ctas, (p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
-  return launch(fa::paged_combine_kernel<D>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, 16 * RB);
+  return launch(fa::paged_combine_kernel<D, kQuant>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, C::kRows);
 }
 
 template <int D, bool kQuant>
-fa_status launch_paged_rows(const fa::PagedParams& p, int ctas, cudaStream_t st) {
-  if (p.R <= 16) return launch_paged<D, kQuant, 1>(p, ctas, st);
-  if (p.R <= 32) return launch_paged<D, kQuant, 2>(p, ctas, st);
-  return launch_paged<D, kQuant, 4>(p, ctas, st);
+fa_status launch_paged_rows(const fa::PagedParams& p, double tiles, cudaStream_t st) {
+  switch (paged_rows(p.R)) {
+    case 8: return launch_paged<D, kQuant, 1, 1>(p, tiles, st);
+    case 16: return launch_paged<D, kQuant, 2, 1>(p, tiles, st);
+    case 32: return launch_paged<D, kQuant, 2, 2>(p, tiles, st);
+    default: return launch_paged<D, kQuant, 2, 4>(p, tiles, st);
+  }
 }
 
 bool paged_sizes_ok(int B, int H, int Hkv, int Nq) {
@@ -238,7 +246,7 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.window = window < (1 << 30) ? window : -1;  // positions stay below 2^30
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   p.R = p.g * Nq;
-  const int block = p.R <= 16 ? 16 : p.R <= 32 ? 32 : 64;
+  const int block = paged_rows(p.R);
   p.nblk = (p.R + block - 1) / block;
   p.prow = std::min(p.R, block);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -246,14 +254,12 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.split = reinterpret_cast<int4*>(ws);
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
-  // no more CTAs than the lengths could give tiles
   const long long cap = static_cast<long long>(cache->max_pages) * cache->page_size;
   const double tiles = static_cast<double>((cap + fa::kPagedTile - 1) / fa::kPagedTile) * B * Hkv * p.nblk;
-  if (tiles / fa::kPagedMaxCtas > 1e9) return FA_ERR_UNSUPPORTED;  // a CTA counts its tiles in 32 bits
-  const int ctas = static_cast<int>(std::min<double>(fa::kPagedMaxCtas, tiles));
+  if (tiles / 148 > 1e9) return FA_ERR_UNSUPPORTED;  // a CTA counts its tiles in 32 bits
   const bool quant = cache->dtype == FA_CACHE_E4M3;
-  if (d == 64) return quant ? launch_paged_rows<64, true>(p, ctas, st) : launch_paged_rows<64, false>(p, ctas, st);
-  return quant ? launch_paged_rows<128, true>(p, ctas, st) : launch_paged_rows<128, false>(p, ctas, st);
+  if (d == 64) return quant ? launch_paged_rows<64, true>(p, tiles, st) : launch_paged_rows<64, false>(p, tiles, st);
+  return quant ? launch_paged_rows<128, true>(p, tiles, st) : launch_paged_rows<128, false>(p, tiles, st);
 }
 
 }  // extern "C"

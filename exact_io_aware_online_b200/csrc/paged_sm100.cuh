@@ -9,8 +9,10 @@
 //
 // What bounds it: every key and value crosses HBM once and meets the g * Nq
 // rows that share its kv head, 2 * rows flops a byte (bf16): below 64 rows far
-// under what mma.sync delivers, so the kernel is laid out for bytes in flight,
-// not for the tensor pipe.  Rows are padded to 16 for m16n8k16 products.
+// under what mma.sync delivers, so the kernel is laid out for bytes in flight
+// and few instructions, not for the tensor pipe.  Both products are formed
+// transposed, S^T = K Q^T and O^T = V^T P^T, so that the 16 of m16n8k16 is
+// filled by keys and by columns of V and only the rows are padded, to 8.
 //
 // Work: the keys that some row of a unit (sequence, kv head, block of rows) may
 // see are cut into tiles of 64.  All tiles of all units form one list, and CTA
@@ -27,7 +29,7 @@ namespace fa {
 
 constexpr int kPagedTile = 64;      // keys of a tile
 constexpr int kPagedThreads = 128;  // 4 warps
-constexpr int kPagedMaxCtas = 296;  // two on each of 148 SMs
+constexpr int kPagedMaxCtas = 444;  // three on each of 148 SMs
 constexpr int kPagedCombineRows = 8;
 constexpr int kPagedRing = 8;       // descriptions of tiles: those staged, the one computed and the next one
 
@@ -40,26 +42,30 @@ struct PagedParams {
   int H, Nq, g;  // g = H / Hkv
   float scale_log2;
   int causal, window;
-  int R, nblk;     // rows of a kv head (g * Nq), blocks of 16 * RB rows they make
-  int prow;        // rows of a partial: min(R, 16 * RB)
+  int R, nblk;     // rows of a kv head (g * Nq), units they make
+  int prow;        // rows of a partial: min(R, rows of a unit)
   float* part_o;   // [2 * G][prow][D]
-  float4* part_m;  // [2 * G][prow]: m, l, sum of the weights as the second product saw them
+  float4* part_m;  // [2 * G][prow]: m, l, unit of the accumulator
   int4* split;     // [G]: the unit that starts in CTA c and goes on in later ones: b, unit, CTAs it spans (or 0)
 };
 
-template <int D, bool kQuant, int RB>
+// A warp holds NB blocks of 8 rows; RG groups of warps hold different rows, the
+// 4 / RG warps of a group share each tile's keys.
+template <int D, bool kQuant, int NB, int RG>
 struct PagedCfg {
+  static constexpr int kRows = 8 * NB * RG;  // rows of a unit
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
   static constexpr int kTileBytes = kPagedTile * kRowBytes;
   static constexpr int kScaleBytes = kQuant ? kPagedTile * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + 2 * kScaleBytes;
-  // stages: as many as two CTAs of an SM have room for
-  static constexpr int kStages = kStageBytes >= 32768 ? 3 : 5;
-  static constexpr int kMerge = 4 * 16 * 8 * 16;  // 4 warps x 16 rows x 8 groups of 4 floats
+  static constexpr int kCtas = kStageBytes >= 32768 || (D == 128 && NB == 2) ? 2 : 3;  // of an SM
+  static constexpr int kStages = kStageBytes >= 32768 || (kStageBytes >= 16384 && kCtas == 3) ? 3 : 5;
+  static constexpr int kMergeStride = D + 4;  // floats; 2 * stride = 8 mod 32: a warp's stores meet every bank once
+  static constexpr int kStatBytes = 4 * 8 * NB * 16;
   static constexpr int kOffsBytes = kPagedRing * kPagedTile * 8;
-  static constexpr int kSmemBytes =
-      kStages * kStageBytes + kMerge + 4 * 16 * 16 + (kQuant ? 2 : 1) * kOffsBytes + kPagedRing * 32;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kStatBytes + (kQuant ? 2 : 1) * kOffsBytes + kPagedRing * 32;
   static_assert(kStages + 2 <= kPagedRing, "a tile's description outlives its copies");
+  static_assert(4 * 8 * kMergeStride * 4 <= kStageBytes, "the warps' accumulators are joined in a stage");
 };
 
 __device__ __forceinline__ uint32_t paged_smem(const void* p) {
@@ -86,37 +92,65 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 y = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
-// Two e4m3 codes as two bf16 numbers (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t x) {
-  const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(x));
-  return pack_bf16(f.x, f.y);
+// c[16 x 8] += a[16 x 16] b[16 x 8]; a, b both f16 or both bf16.
+template <bool kHalf>
+__device__ __forceinline__ void mma16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t* b) {
+  if (kHalf)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+// The transpose of an 8 x 8 matrix of 16-bit values, a row per four lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// Two e4m3 codes (the low one first) as two f16 numbers (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 
-// 16-byte unit `chunk` of key row `key` of a staged tile.  The exponent-or
-// spreads both access patterns over all banks: keys (2m, 2m + 1) x 4 units (K)
-// and keys (2q + const, q = 0..3) x 2 units (V).
+// Byte of the 16-byte unit `chunk` of key row `key` in a staged tile.  K: eight
+// lanes read keys (2m, 2m + 1) x 4 consecutive units.  V: bf16, eight keys x
+// one unit (ldmatrix); e4m3, keys (0, 2, 4, 6) + const x units (2c, 2c + 1).
+// The exclusive-or puts each such set into different banks (but for V rows of
+// 64 bytes, which are read in pairs).
 template <int kRowBytes>
-__device__ __forceinline__ uint32_t paged_at(int key, int chunk) {
-  const int hi = (((key >> 2) ^ key) & 1) << 2;
-  if (kRowBytes == 256) return key * 256 + ((chunk ^ (((key >> 1) & 1) | hi)) << 4);
-  if (kRowBytes == 128) return key * 128 + ((chunk ^ ((((key >> 1) & 1) << 1) | hi)) << 4);
-  return key * 64 + ((chunk ^ (((key >> 1) & 1) << 1)) << 4);
+__device__ __forceinline__ uint32_t k_at(int key, int chunk) {
+  return key * kRowBytes + (kRowBytes == 64 ? chunk << 4 : (chunk ^ ((key & 1) << 2)) << 4);
+}
+template <int kRowBytes, bool kQuant>
+__device__ __forceinline__ uint32_t v_at(int key, int chunk) {
+  const int x = !kQuant ? key & 7 : kRowBytes == 128 ? key & 6 : key & 2;
+  return key * kRowBytes + ((chunk ^ x) << 4);
 }
 
 // First key that some row of a sequence of length L may see, and its tiles.
@@ -134,27 +168,27 @@ struct PagedDesc {  // a tile, as the front of the pipeline describes it to the 
 };
 constexpr int kFlagUnitStart = 1, kFlagUnitEnd = 2, kFlagSegEnd = 4;
 
-template <int D, bool kQuant, int RB>
-__global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedParams p) {
-  using C = PagedCfg<D, kQuant, RB>;
-  constexpr int KW = 4 / RB;           // warps that share a row block's keys
-  constexpr int NT = D / 8;            // output column tiles
-  constexpr int QS = D / 16;           // k-steps of the score product
-  constexpr int ST = C::kStages;
+template <int D, bool kQuant, int NB, int RG>
+__global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kCtas)
+    paged_kernel(const PagedParams p) {
+  using C = PagedCfg<D, kQuant, NB, RG>;
+  constexpr int KW = 4 / RG;                  // warps that share a tile's keys
+  constexpr int DT = D / 16;                  // row tiles of O^T = V^T P^T
+  constexpr int QS = D / 16;                  // k-steps of S^T = K Q^T
+  constexpr int ST = C::kStages, RB = C::kRowBytes;
   constexpr int ES = kQuant ? 1 : 2;
-  extern __shared__ __align__(128) uint8_t smem[];
-  float4* merge = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);
-  float4* stat = merge + 4 * 16 * 8;                                   // [4 warps][16 rows]: m, l, lb
-  long long* offs = reinterpret_cast<long long*>(stat + 4 * 16);       // [ring][64] element offset of a row, -1: none
-  long long* soffs = offs + kPagedRing * kPagedTile;                   // [ring][64] offset of its scale
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float4* stat = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);  // [4 warps][8 * NB rows]: m, l, unit
+  long long* offs = reinterpret_cast<long long*>(stat + 4 * 8 * NB);     // [ring][64] element offset of a row, -1: none
+  long long* soffs = offs + kPagedRing * kPagedTile;                     // [ring][64] offset of its scale
   PagedDesc* desc = reinterpret_cast<PagedDesc*>(kQuant ? soffs + kPagedRing * kPagedTile : soffs);  // [ring]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, B = p.c.B;
-  const long long U = static_cast<long long>(p.c.Hkv) * p.nblk;  // units of a sequence
+  const int U = p.c.Hkv * p.nblk;  // units of a sequence
 
   // ---- this CTA's share [t0, t1) of the tile list
-  long long* red = reinterpret_cast<long long*>(merge);
+  long long* red = reinterpret_cast<long long*>(smem);
   long long sum = 0;
   for (int b = tid; b < B; b += kPagedThreads) sum += paged_tiles(p, cache_length(p.c, b));
 #pragma unroll
@@ -188,7 +222,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
     long long base = 0;
     for (int at = 0;; at += kPagedThreads) {
       const int b = at + tid;
-      const long long mine = b < B ? paged_tiles(p, cache_length(p.c, b)) * U : 0;
+      const long long mine = b < B ? static_cast<long long>(paged_tiles(p, cache_length(p.c, b))) * U : 0;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -218,29 +252,30 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
     ft = static_cast<int>(off % fnt);
     fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
   }
-  // what fetch() leaves for store()
-  int n_page = -1, n_slot = 0, n_b = 0, n_u = 0, n_key0 = 0, n_flags = 0, n_L = 0;
   const int frow = tid & (kPagedTile - 1);
+  struct Tile {  // a tile as fetch() leaves it for store(): this thread's row
+    int page, slot, b, u, key0, flags, L;
+  };
 
   // fetch(n): loads the page of this thread's row of tile n and advances the cursor
   auto fetch = [&](int n) {
-    if (n >= cnt) return;
-    n_b = fb;
-    n_u = fu;
-    n_L = fL;
-    n_key0 = paged_first_key(p, fL) + ft * kPagedTile;
-    n_flags = (ft == 0 ? kFlagUnitStart : 0) | (ft == fnt - 1 ? kFlagUnitEnd | kFlagSegEnd : 0) |
+    Tile t = {-1, 0, 0, 0, 0, 0, 0};
+    if (n >= cnt) return t;
+    t.b = fb;
+    t.u = fu;
+    t.L = fL;
+    t.key0 = paged_first_key(p, fL) + ft * kPagedTile;
+    t.flags = (ft == 0 ? kFlagUnitStart : 0) | (ft == fnt - 1 ? kFlagUnitEnd | kFlagSegEnd : 0) |
               (n == cnt - 1 ? kFlagSegEnd : 0);
-    const int pos = n_key0 + frow;
-    n_page = -1;
+    const int pos = t.key0 + frow;
     if (pos < fL) {
       const int i = pos / p.c.page_size;
-      n_slot = pos - i * p.c.page_size;
-      n_page = p.c.table[fb * p.c.table_stride + i];
+      t.slot = pos - i * p.c.page_size;
+      t.page = p.c.table[fb * p.c.table_stride + i];
     }
     if (++ft == fnt) {
       ft = 0;
-      if (++fu == static_cast<int>(U)) {
+      if (++fu == U) {
         fu = 0;
         if (n + 1 < cnt) {  // the next sequence with keys (there is one: tiles are left)
           do {
@@ -252,44 +287,45 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
         }
       }
     }
+    return t;
   };
   // store(n): the row's offsets and the tile's description, for issue() and compute()
-  auto store = [&](int n) {
+  auto store = [&](int n, const Tile& f) {
     if (n >= cnt) return;
-    const bool on = n_page >= 0 && n_page < p.c.num_pages;
-    const int kh = n_u / p.nblk;
+    const bool on = f.page >= 0 && f.page < p.c.num_pages;
+    const int kh = p.nblk == 1 ? f.u : f.u / p.nblk;
     if (tid < kPagedTile) {
-      offs[(n % kPagedRing) * kPagedTile + frow] = on ? p.c.pages.row(n_page, kh, n_slot) : -1;
+      offs[(n % kPagedRing) * kPagedTile + frow] = on ? p.c.pages.row(f.page, kh, f.slot) * ES : -1;
       const uint32_t m = __ballot_sync(0xffffffffu, on);
       PagedDesc& t = desc[n % kPagedRing];
       if (lane == 0) t.valid[warp] = m;
       if (tid == 0) {
-        t.b = n_b;
-        t.unit = n_u;
-        t.key0 = n_key0;
-        t.flags = n_flags;
-        t.L = n_L;
+        t.b = f.b;
+        t.unit = f.u;
+        t.key0 = f.key0;
+        t.flags = f.flags;
+        t.L = f.L;
       }
     } else if (kQuant) {
-      soffs[(n % kPagedRing) * kPagedTile + frow] = on ? p.c.scales.row(n_page, kh, n_slot) : -1;
+      soffs[(n % kPagedRing) * kPagedTile + frow] = on ? p.c.scales.row(f.page, kh, f.slot) : -1;
     }
   };
   const uint32_t smem0 = paged_smem(smem);
   // issue(n): the copies of tile n into its stage (always one group, empty past the end)
+  constexpr int CPR = RB / 16, RPI = kPagedThreads / CPR;  // 16-byte units of a row, rows of a pass
+  const int chunk = tid % CPR, crow = tid / CPR;
   auto issue = [&](int n) {
     if (n < cnt) {
-      constexpr int CPR = C::kRowBytes / 16, RPI = kPagedThreads / CPR;  // units of a row, rows of a pass
       const uint32_t dst = smem0 + (n % ST) * C::kStageBytes;
-      const int chunk = tid % CPR;
+      const long long* src = offs + (n % kPagedRing) * kPagedTile + crow;
 #pragma unroll
       for (int i = 0; i < kPagedTile / RPI; ++i) {
-        const int row = tid / CPR + i * RPI;
-        const long long off = offs[(n % kPagedRing) * kPagedTile + row];
+        const int row = crow + i * RPI;
+        const long long off = src[i * RPI];
         const bool on = off >= 0;
-        const long long at = (on ? off * ES : 0) + chunk * 16;
-        const uint32_t to = dst + paged_at<C::kRowBytes>(row, chunk);
-        cp_async16(to, p.c.k + at, on);
-        cp_async16(to + C::kTileBytes, p.c.v + at, on);
+        const long long at = (on ? off : 0) + chunk * 16;
+        cp_async16(dst + k_at<RB>(row, chunk), p.c.k + at, on);
+        cp_async16(dst + C::kTileBytes + v_at<RB, kQuant>(row, chunk), p.c.v + at, on);
       }
       if (kQuant) {
         const long long off = soffs[(n % kPagedRing) * kPagedTile + frow];
@@ -301,78 +337,109 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
   };
 
   // ---- a warp's rows and its share of a tile's keys
-  const int rb = warp / KW, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
-  uint32_t qa[QS][4];
-  float acc[NT][4];
-  float m[2], l[2], lb[2];
-  int rlo[2], rhi[2];          // keys that the thread's two rows may see
+  const int rg = warp / KW, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
+  uint32_t qb[NB][QS][2];  // Q^T: row rq of each block, the k index in the order in which a key's 16-byte units come
+  float acc[NB][DT][4];    // O^T: columns dcol(x, 0), dcol(x, 1) of V for rows 2 qd, 2 qd + 1
+  float m[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2];
+  int rlo[NB][2], rhi[NB][2];  // keys that the thread's rows may see
   int free_lo = 0, free_hi = 0;  // keys that every row of the unit may see
-  bool seg_starts_unit = false;
+  bool seg_starts_unit = false, fresh = true;  // fresh: the next tile begins a segment
   int seg_first = 0;
-  bool fresh = true;  // the next tile begins a segment
+  auto dcol = [&](int x, int e) { return kQuant ? rq * (D / 8) + 2 * x + e : 16 * x + 8 * e + rq; };
+  // the queries of unit t, as they are in memory
+  auto load_q = [&](const PagedDesc& t) {
+    const int kh = p.nblk == 1 ? t.unit : t.unit / p.nblk, row0 = (t.unit - kh * p.nblk) * C::kRows + rg * 8 * NB;
+    constexpr int W2 = kQuant ? 8 : 4;  // words of q that belong to one 16-byte unit of k
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = row0 + nb * 8 + rq;
+      const int h = p.Nq == 1 ? r : r / p.Nq;
+      const uint8_t* qr = p.q + 2 * (r < p.R ? p.sq.row(t.b, kh * p.g + h, r - h * p.Nq) : 0);
+#pragma unroll
+      for (int i = 0; i < D / 2 / W2 / 4; ++i)
+#pragma unroll
+        for (int y = 0; y < W2; y += 4) {
+          const uint4 v = r < p.R ? __ldg(reinterpret_cast<const uint4*>(qr + (qd + 4 * i) * W2 * 4 + y * 4))
+                                  : make_uint4(0, 0, 0, 0);
+          const int s = i * (W2 / 2) + y / 2;
+          qb[nb][s][0] = v.x;
+          qb[nb][s][1] = v.y;
+          qb[nb][s + 1][0] = v.z;
+          qb[nb][s + 1][1] = v.w;
+        }
+    }
+  };
 
-  for (int n = 0; n < ST; ++n) {
-    fetch(n);
-    store(n);
+  {
+    Tile t[ST];
+#pragma unroll
+    for (int n = 0; n < ST; ++n) t[n] = fetch(n);
+#pragma unroll
+    for (int n = 0; n < ST; ++n) store(n, t[n]);
   }
-  fetch(ST);
   __syncthreads();
+#pragma unroll
   for (int n = 0; n < ST - 1; ++n) issue(n);
+  load_q(desc[0]);
+  Tile next = fetch(ST);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   for (int n = 0; n < cnt; ++n) {
     cp_async_wait<ST - 2>();
-    store(n + ST);
+    store(n + ST, next);
     __syncthreads();  // tile n has landed; everyone is done with tile n - 1
     issue(n + ST - 1);
-    fetch(n + ST + 1);
+    next = fetch(n + ST + 1);
 
     const PagedDesc& t = desc[n % kPagedRing];
-    const int b = t.b, unit = t.unit, key0 = t.key0, flags = t.flags;
-    const int kh = unit / p.nblk, row0 = (unit % p.nblk) * 16 * RB;
+    const int key0 = t.key0, flags = t.flags;
     if (fresh) {
       fresh = false;
       seg_starts_unit = flags & kFlagUnitStart;
       seg_first = n;
-      const int L = t.L;
+      const int L = t.L, row0 = (p.nblk == 1 ? 0 : t.unit % p.nblk * C::kRows) + rg * 8 * NB;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        m[x] = -INFINITY;
-        l[x] = lb[x] = 0.f;
-        const int r = row0 + rb * 16 + rq + 8 * x;
-        const int h = r / p.Nq, i = r - h * p.Nq, pos = L - p.Nq + i;
-        const bool on = r < p.R;
-        rlo[x] = 0;
-        rhi[x] = 0x7fffffff;  // padding rows: never stored
-        if (on) {
-          rlo[x] = p.window < 0 ? 0 : max(0, pos - p.window);
-          rhi[x] = pos < 0 ? 0 : (p.causal ? pos + 1 : (p.window < 0 ? L : min(L, pos + p.window + 1)));
+      for (int nb = 0; nb < NB; ++nb) {
+        float back = p.scale_log2;  // what a product of the scaled queries is multiplied by
+        if (kQuant) {
+          // bf16 queries as f16: scaled by a power of two that puts the row's
+          // largest into [2^14, 2^15); exact down to 2^-32 of it
+          uint32_t mx = 0;
+#pragma unroll
+          for (int s = 0; s < QS; ++s)
+            mx = __vmaxu2(mx, __vmaxu2(qb[nb][s][0] & 0x7fff7fffu, qb[nb][s][1] & 0x7fff7fffu));
+          mx = max(mx & 0xffffu, mx >> 16);
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const uint32_t e = min(max(mx >> 7, 27u), 254u);
+          const float up = __uint_as_float((268u - e) << 23);
+          back *= __uint_as_float((e - 14u) << 23);
+#pragma unroll
+          for (int s = 0; s < QS; ++s)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              qb[nb][s][y] = pack_f16(__uint_as_float(qb[nb][s][y] << 16) * up,
+                                      __uint_as_float(qb[nb][s][y] & 0xffff0000u) * up);
         }
-        const uint8_t* qr = p.q + 2 * (on ? p.sq.row(b, kh * p.g + h, i) : 0);
-        // the k index of the score product is permuted so that a key's row is
-        // read in 16-byte units; the queries take the same order
-        constexpr int W2 = kQuant ? 8 : 4;  // words of q that belong to one 16-byte unit of k
 #pragma unroll
-        for (int i2 = 0; i2 < D / (8 * W2); ++i2) {
-          uint32_t w[W2];
-#pragma unroll
-          for (int y = 0; y < W2; y += 4) {
-            const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(qr + (qd + 4 * i2) * W2 * 4 + y * 4))
-                               : make_uint4(0, 0, 0, 0);
-            w[y] = v.x;
-            w[y + 1] = v.y;
-            w[y + 2] = v.z;
-            w[y + 3] = v.w;
-          }
-#pragma unroll
-          for (int y = 0; y < W2 / 2; ++y) {
-            qa[i2 * (W2 / 2) + y][x] = w[2 * y];
-            qa[i2 * (W2 / 2) + y][2 + x] = w[2 * y + 1];
+        for (int c = 0; c < 2; ++c) {
+          m[nb][c] = -INFINITY;
+          l[nb][c] = 0.f;
+          vref[nb][c] = __uint_as_float(1u << 23);   // 2^-126
+          vinv[nb][c] = __uint_as_float(253u << 23);
+          rowf[nb][c] = kQuant ? __shfl_sync(0xffffffffu, back, (2 * qd + c) * 4) : back;
+          const int r = row0 + nb * 8 + 2 * qd + c;
+          const int i = p.Nq == 1 ? 0 : r % p.Nq, pos = L - p.Nq + i;
+          rlo[nb][c] = 0;
+          rhi[nb][c] = 0;  // padding rows see nothing
+          if (r < p.R) {
+            rlo[nb][c] = p.window < 0 ? 0 : max(0, pos - p.window);
+            rhi[nb][c] = pos < 0 ? 0 : (p.causal ? pos + 1 : (p.window < 0 ? L : min(L, pos + p.window + 1)));
           }
         }
+#pragma unroll
+        for (int x = 0; x < DT; ++x) acc[nb][x][0] = acc[nb][x][1] = acc[nb][x][2] = acc[nb][x][3] = 0.f;
       }
-#pragma unroll
-      for (int x = 0; x < NT; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
       free_lo = p.window < 0 ? 0 : max(0, L - 1 - p.window);
       free_hi = L < p.Nq ? 0 : (p.causal ? L - p.Nq + 1 : (p.window < 0 ? L : min(L, L - p.Nq + p.window + 1)));
     }
@@ -381,256 +448,286 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
     const float* scl = reinterpret_cast<const float*>(smem + (n % ST) * C::kStageBytes + 2 * C::kTileBytes);
     const bool edge = key0 < free_lo || key0 + kPagedTile > free_hi || (t.valid[0] & t.valid[1]) != 0xffffffffu;
 #pragma unroll 1
-    for (int s = 0; s < RB; ++s) {
-      const int kb = (kw * RB + s) * 16;
-      // ---- scores of 16 keys
-      float sc[2][4];
+    for (int s = 0; s < RG; ++s) {
+      const int kb = (kw * RG + s) * 16;
+      // ---- S^T of keys kb + rq (elements 0, 1) and kb + rq + 8 (2, 3), rows 2 qd and 2 qd + 1
+      float sc[NB][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-        const int key = kb + nt * 8 + rq;
-        if (kQuant) {
+      for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+      if (kQuant) {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const uint4 w = lds128(sK + paged_at<C::kRowBytes>(key, qd + 4 * i));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < D / 64; ++i) {
+          const uint4 a = lds128(sK + k_at<RB>(kb + rq, qd + 4 * i)), b = lds128(sK + k_at<RB>(kb + rq + 8, qd + 4 * i));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_bf16(sc[nt], qa[i * 4 + x], e4m3x2_to_bf16x2(ww[x]), e4m3x2_to_bf16x2(ww[x] >> 16));
-          }
-        } else {
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t a0 = e4m3x2_to_f16x2(aw[x] & 0xffffu), a2 = e4m3x2_to_f16x2(aw[x] >> 16),
+                           a1 = e4m3x2_to_f16x2(bw[x] & 0xffffu), a3 = e4m3x2_to_f16x2(bw[x] >> 16);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint4 w = lds128(sK + paged_at<C::kRowBytes>(key, qd + 4 * i));
-            mma_bf16(sc[nt], qa[2 * i], w.x, w.y);
-            mma_bf16(sc[nt], qa[2 * i + 1], w.z, w.w);
+            for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[nb], a0, a1, a2, a3, qb[nb][i * 4 + x]);
           }
         }
-      }
-      float2 vs[2];
+      } else {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float2 f = make_float2(p.scale_log2, p.scale_log2);
-        if (kQuant) {
-          const float2 ks = *reinterpret_cast<const float2*>(scl + kb + nt * 8 + 2 * qd);
-          vs[nt] = *reinterpret_cast<const float2*>(scl + kPagedTile + kb + nt * 8 + 2 * qd);
-          f.x *= ks.x;
-          f.y *= ks.y;
-        }
-        sc[nt][0] *= f.x;
-        sc[nt][1] *= f.y;
-        sc[nt][2] *= f.x;
-        sc[nt][3] *= f.y;
-      }
-      uint32_t allowed = 0xff;  // bit nt * 4 + e
-      if (edge) {
-        allowed = 0;
-        const uint32_t vm = t.valid[kb >> 5] >> (kb & 31);
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 a = lds128(sK + k_at<RB>(kb + rq, qd + 4 * i)), b = lds128(sK + k_at<RB>(kb + rq + 8, qd + 4 * i));
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = nt * 8 + 2 * qd + (e & 1), j = key0 + kb + k;
-            if (((vm >> k) & 1) && j >= rlo[e >> 1] && j < rhi[e >> 1])
-              allowed |= 1u << (nt * 4 + e);
-            else
-              sc[nt][e] = -INFINITY;
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16<false>(sc[nb], a.x, b.x, a.y, b.y, qb[nb][2 * i]);
+            mma16<false>(sc[nb], a.z, b.z, a.w, b.w, qb[nb][2 * i + 1]);
           }
-      }
-      // ---- running maximum: moved only when it grows by more than 8 (weights stay below 2^8)
-      float mx[2] = {fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])),
-                     fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]))};
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
-        float f[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-          const float mn = mx[x] > m[x] + 8.f ? mx[x] : m[x];
-          f[x] = m[x] == mn ? 1.f : exp2_fast(m[x] - mn);
-          m[x] = mn;
-          l[x] *= f[x];
-          lb[x] *= f[x];
-        }
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          acc[x][0] *= f[0];
-          acc[x][1] *= f[0];
-          acc[x][2] *= f[1];
-          acc[x][3] *= f[1];
         }
       }
-      const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-      uint32_t pa[4];
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+      if (kQuant) {
+        ks[0] = scl[kb + rq];
+        ks[1] = scl[kb + rq + 8];
+        vs[0] = scl[kPagedTile + kb + rq];
+        vs[1] = scl[kPagedTile + kb + rq + 8];
+      }
+      uint32_t allowed = 0xffffffffu;  // bit 4 nb + e
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float w[4];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          w[e] = exp2_fast(sc[nt][e] - mu[e >> 1]);
-          l[e >> 1] += w[e];
-          if (kQuant) w[e] = edge && !((allowed >> (nt * 4 + e)) & 1) ? 0.f : w[e] * ((e & 1) ? vs[nt].y : vs[nt].x);
+          sc[nb][e] *= rowf[nb][e & 1];
+          if (kQuant) sc[nb][e] *= ks[e >> 1];
         }
-        // the weights are rounded to bf16 for the second product (half a step,
-        // 2^-8 of a weight); unquantised rows are normalised by the sum of the
-        // rounded weights, so that O stays a mean of value rows
-        pa[nt * 2] = pack_bf16(w[0], w[1]);
-        pa[nt * 2 + 1] = pack_bf16(w[2], w[3]);
-        if (!kQuant)
+      if (edge) {
+        const uint32_t vm = t.valid[kb >> 5] >> (kb & 31);
+        allowed = 0;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            lb[x] += __uint_as_float(pa[nt * 2 + x] << 16) + __uint_as_float(pa[nt * 2 + x] & 0xffff0000u);
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = rq + 8 * (e >> 1), j = key0 + kb + k;
+            if (((vm >> k) & 1) && j >= rlo[nb][e & 1] && j < rhi[nb][e & 1])
+              allowed |= 1u << (4 * nb + e);
+            else
+              sc[nb][e] = -INFINITY;
+          }
       }
-      // ---- O += P V: output column x + NT * rq of thread column pair is tile x, so that a
-      // thread reads D / 8 consecutive values of each of its four keys
-      const int vk[4] = {kb + 2 * qd, kb + 2 * qd + 1, kb + 2 * qd + 8, kb + 2 * qd + 9};
-      uint32_t bad = 0;
+      // ---- running maximum: moved only when it grows by more than 8 (weights
+      // stay below 2^8).  Quantised: weights reach the second product as f16
+      // multiples of the largest value scale so far (vref, a power of two above
+      // it); a row's accumulator counts in units of its vref.
+      bool grow = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          grow |= fmaxf(sc[nb][c], sc[nb][2 + c]) > m[nb][c] + 8.f;
+          if (kQuant)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              grow |= fabsf(vs[h]) >= vref[nb][c] && ((allowed >> (4 * nb + 2 * h + c)) & 1);
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(sc[nb][c], sc[nb][2 + c]);
+            uint32_t ve = 0;
+            if (kQuant)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if ((allowed >> (4 * nb + 2 * h + c)) & 1) ve = max(ve, (__float_as_uint(vs[h]) >> 23) & 0xffu);
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              if (kQuant) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, o));
+            }
+            const float mn = mx > m[nb][c] + 8.f ? mx : m[nb][c];
+            float f = m[nb][c] == mn ? 1.f : exp2_fast(m[nb][c] - mn);
+            m[nb][c] = mn;
+            l[nb][c] *= f;
+            if (kQuant) {
+              const float vn = fmaxf(vref[nb][c], __uint_as_float(min(ve + 1u, 253u) << 23));
+              vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
+              f *= vref[nb][c] * vinv[nb][c];
+              vref[nb][c] = vn;
+            }
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {
+              acc[nb][x][c] *= f;
+              acc[nb][x][2 + c] *= f;
+            }
+          }
+      }
+      // The weights are rounded to 16 bits for the second product: bf16 (half a
+      // step is 2^-8 of a weight), or f16 of weight * value scale / vref, 2^-11
+      // of it down to 2^-14; rows that hold a scale below 2^-12 vref take the
+      // slow form below.
+      uint32_t pb[NB][2];
+      bool slow = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mu = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
+          const float w = exp2_fast(sc[nb][e] - mu);
+          l[nb][e & 1] += w;
+          sc[nb][e] = w;
+          if (kQuant) {
+            const float u = vs[e >> 1] * vinv[nb][e & 1];
+            const bool on = (allowed >> (4 * nb + e)) & 1;
+            slow |= on && fabsf(u) < 0x1p-12f && fabsf(vs[e >> 1]) > 0x1p-90f;
+            sc[nb][e] = on ? w * u : 0.f;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pb[nb][h] = transpose8x8(kQuant ? pack_f16(sc[nb][2 * h], sc[nb][2 * h + 1])
+                                          : pack_bf16(sc[nb][2 * h], sc[nb][2 * h + 1]));
+      }
+      // ---- O^T += V^T P^T
+      uint32_t bad = slow;
       if (kQuant) {
         uint32_t w[4][D / 32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          const int key = kb + 2 * qd + (k & 1) + 8 * (k >> 1);
           if (D == 128) {
-            const uint4 v = lds128(sV + paged_at<C::kRowBytes>(vk[k], rq));
+            const uint4 v = lds128(sV + v_at<RB, kQuant>(key, rq));
             w[k][0] = v.x;
             w[k][1] = v.y;
             w[k][2 % (D / 32)] = v.z;
             w[k][3 % (D / 32)] = v.w;
           } else {
-            const uint2 v = lds64(sV + paged_at<C::kRowBytes>(vk[k], rq >> 1) + (rq & 1) * 8);
+            const uint2 v = lds64(sV + v_at<RB, kQuant>(key, rq >> 1) + (rq & 1) * 8);
             w[k][0] = v.x;
             w[k][1] = v.y;
           }
         }
-        uint32_t vb[2][NT];
-#pragma unroll
-        for (int x = 0; x < NT / 2; ++x) {  // codes 2x, 2x + 1 of the thread's columns
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t z = __byte_perm(w[2 * y][x >> 1], w[2 * y + 1][x >> 1], (x & 1) ? 0x7362 : 0x5140);
-            vb[y][2 * x] = e4m3x2_to_bf16x2(z);
-            vb[y][2 * x + 1] = e4m3x2_to_bf16x2(z >> 16);
-          }
-        }
-        if (edge)
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              bad |= ((vb[y][x] & 0x7f80u) == 0x7f80u) | ((vb[y][x] & 0x7f800000u) == 0x7f800000u);
-        if (!edge || !__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-          for (int x = 0; x < NT; ++x) mma_bf16(acc[x], pa, vb[0][x], vb[1][x]);
-          continue;
-        }
-      } else {
-        uint32_t w[4][D / 16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int y = 0; y < D / 64; ++y) {
-            const uint4 v = lds128(sV + paged_at<C::kRowBytes>(vk[k], rq * (D / 64) + y));
-            w[k][4 * y] = v.x;
-            w[k][4 * y + 1] = v.y;
-            w[k][4 * y + 2] = v.z;
-            w[k][4 * y + 3] = v.w;
-          }
         if (edge)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int y = 0; y < D / 16; ++y)
-              bad |= ((w[k][y] & 0x7f80u) == 0x7f80u) | ((w[k][y] & 0x7f800000u) == 0x7f800000u);
+            for (int y = 0; y < D / 32; ++y) bad |= ((w[k][y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // NaN codes
+        if (!__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+          for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
+            const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
+            const uint32_t lo = __byte_perm(w[0][x >> 1], w[1][x >> 1], sel), hi = __byte_perm(w[2][x >> 1], w[3][x >> 1], sel);
+            const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xffffu), a1 = e4m3x2_to_f16x2(lo >> 16),
+                           a2 = e4m3x2_to_f16x2(hi & 0xffffu), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[nb]);
+          }
+          continue;
+        }
+      } else {
+        const int key = kb + (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t at = sV + v_at<RB, kQuant>(key, (lane >> 3) & 1);
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < DT; ++x) {
+            uint32_t a[4];
+            ldmatrix_x4_trans(a, at ^ (x << 5));
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              bad |= ((a[y] & 0x7f80u) == 0x7f80u) | ((a[y] & 0x7f800000u) == 0x7f800000u);
+          }
+        }
         if (!edge || !__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            const uint32_t sel = (x & 1) ? 0x7632 : 0x5410;
-            mma_bf16(acc[x], pa, __byte_perm(w[0][x >> 1], w[1][x >> 1], sel),
-                     __byte_perm(w[2][x >> 1], w[3][x >> 1], sel));
+          for (int x = 0; x < DT; ++x) {
+            uint32_t a[4];
+            ldmatrix_x4_trans(a, at ^ (x << 5));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x], a[0], a[1], a[2], a[3], pb[nb]);
           }
           continue;
         }
       }
-      // An infinity or NaN among the values of a tile that some rows see only in
-      // part: 0 * infinity would reach rows that may not see that key, so the
-      // products are formed one by one and weights of zero are left out.
+      // The slow form: products one by one in fp32, weights of zero left out.
+      // For an infinity or NaN among the values of a tile that some rows see
+      // only in part (0 * infinity would reach rows that may not see that key),
+      // and for value scales too far apart for f16.
 #pragma unroll 1
-      for (int k = 0; k < 16; ++k) {
-        const int src = (lane & ~3) | ((k & 7) >> 1);
-        const uint32_t w0 = __shfl_sync(0xffffffffu, k < 8 ? pa[0] : pa[2], src);
-        const uint32_t w1 = __shfl_sync(0xffffffffu, k < 8 ? pa[1] : pa[3], src);
-        const float f0 = __uint_as_float((k & 1) ? w0 & 0xffff0000u : w0 << 16);
-        const float f1 = __uint_as_float((k & 1) ? w1 & 0xffff0000u : w1 << 16);
+      for (int k = 0; k < 16; ++k)
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+        for (int nb = 0; nb < NB; ++nb) {
+          const int src = (k & 7) * 4 + qd;
+          const float f0 = __shfl_sync(0xffffffffu, k < 8 ? sc[nb][0] : sc[nb][2], src);
+          const float f1 = __shfl_sync(0xffffffffu, k < 8 ? sc[nb][1] : sc[nb][3], src);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int col = (2 * qd + e) * NT + x;
-            const uint32_t at = sV + paged_at<C::kRowBytes>(kb + k, col * ES / 16) + (col * ES) % 16;
-            float v;
-            if (kQuant) {
+          for (int x = 0; x < DT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int col = dcol(x, e);
+              const uint32_t at = sV + v_at<RB, kQuant>(kb + k, col * ES / 16) + (col * ES) % 16;
               uint32_t z;
-              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(at));
-              v = e4m3x2_to_float2(static_cast<uint16_t>(z)).x;
-            } else {
-              uint32_t z;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=r"(z) : "r"(at));
-              v = __uint_as_float(z << 16);
+              float v;
+              if (kQuant) {
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
+                v = e4m3x2_to_float2(static_cast<uint16_t>(z)).x;
+              } else {
+                asm volatile("ld.shared.u16 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
+                v = __uint_as_float(z << 16);
+              }
+              if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
+              if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
             }
-            if (f0 != 0.f) acc[x][e] += f0 * v;
-            if (f1 != 0.f) acc[x][2 + e] += f1 * v;
-          }
-      }
+        }
     }
 
     if (!(flags & kFlagSegEnd)) continue;
-    // ---- the segment's end: the KW warps of a row block join their states
+    // ---- the segment's end: the KW warps of a row group join their states in tile n's stage
     fresh = true;
+    const int b = t.b, unit = t.unit, L = t.L;
+    const int kh = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - kh * p.nblk) * C::kRows;
     const bool whole = seg_starts_unit && (flags & kFlagUnitEnd);
     const int slot = 2 * cta + (seg_starts_unit ? 1 : 0);
+    if (n + 1 < cnt) load_q(desc[(n + 1) % kPagedRing]);  // the next unit's queries, on their way meanwhile
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
-        lb[x] += __shfl_xor_sync(0xffffffffu, lb[x], o);
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], o);
+        if (rq == 0) stat[(warp * NB + nb) * 8 + 2 * qd + c] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
       }
-      if (qd == 0) stat[warp * 16 + rq + 8 * x] = make_float4(m[x], l[x], kQuant ? l[x] : lb[x], 0.f);
-    }
-    float out[RB][NT];  // thread: row tid / 8 (+ 16 per item), columns NT * (tid % 8) + 0..NT-1
-    const int orow = tid >> 3, ogrp = tid & 7;
-    float fw[RB][KW], mt[RB], lt[RB], lbt[RB];
+    float* merge = reinterpret_cast<float*>(smem + (n % ST) * C::kStageBytes);  // [4 warps][8 rows][kMergeStride]
 #pragma unroll
-    for (int ps = 0; ps < NT / 4; ++ps) {
-      if (ps) __syncthreads();
+    for (int nb = 0; nb < NB; ++nb) {
+      __syncthreads();  // tile n is read, the block before this one joined
+      float* mine = merge + (warp * 8 + 2 * qd) * C::kMergeStride;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < DT; ++x)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          merge[(warp * 16 + rq + 8 * x) * 8 + ((2 * qd + e) ^ ((rq >> 1) & 3))] =
-              make_float4(acc[4 * ps][2 * x + e], acc[4 * ps + 1][2 * x + e], acc[4 * ps + 2][2 * x + e],
-                          acc[4 * ps + 3][2 * x + e]);
-      __syncthreads();
-#pragma unroll
-      for (int it = 0; it < RB; ++it) {
-        const int w0 = it * KW;
-        if (ps == 0) {
-          mt[it] = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < KW; ++w) mt[it] = fmaxf(mt[it], stat[(w0 + w) * 16 + orow].x);
-          lt[it] = lbt[it] = 0.f;
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            const float4 s4 = stat[(w0 + w) * 16 + orow];
-            fw[it][w] = s4.x == -INFINITY ? (s4.y == 0.f ? 0.f : 1.f) : exp2_fast(s4.x - mt[it]);
-            lt[it] += fw[it][w] * s4.y;
-            lbt[it] += fw[it][w] * s4.z;
+        for (int c = 0; c < 2; ++c)
+          if (kQuant) {
+            *reinterpret_cast<float2*>(mine + c * C::kMergeStride + dcol(x, 0)) =
+                make_float2(acc[nb][x][c], acc[nb][x][2 + c]);
+          } else {
+            mine[c * C::kMergeStride + dcol(x, 0)] = acc[nb][x][c];
+            mine[c * C::kMergeStride + dcol(x, 1)] = acc[nb][x][2 + c];
           }
-        }
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncthreads();
+      constexpr int LPR = D / 4, RPP = kPagedThreads / LPR;  // threads of a row, rows of a pass
+      const int col = tid % LPR * 4;
+#pragma unroll
+      for (int it = 0; it < RG * 8 / RPP; ++it) {
+        const int rr = tid / LPR + it * RPP, g = rr >> 3, r8 = rr & 7;  // row r8 of group g
+        const int rloc = (g * NB + nb) * 8 + r8, r = row0 + rloc;
+        if (r >= p.R) continue;
+        float mt = -INFINITY, vt = 0.f, lt = 0.f;
+        float4 st[KW], a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const float4 v = merge[((w0 + w) * 16 + orow) * 8 + (ogrp ^ ((orow >> 1) & 3))];
-          const float f = fw[it][w];
+          st[w] = stat[((g * KW + w) * NB + nb) * 8 + r8];
+          mt = fmaxf(mt, st[w].x);
+          vt = fmaxf(vt, st[w].z);
+        }
+        const float vti = __uint_as_float((254u << 23) - __float_as_uint(vt));
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          float f = st[w].x == -INFINITY ? (st[w].y == 0.f ? 0.f : 1.f) : exp2_fast(st[w].x - mt);
+          lt += f * st[w].y;
+          if (kQuant) f *= st[w].z * vti;
+          const float4 v = *reinterpret_cast<const float4*>(merge + ((g * KW + w) * 8 + r8) * C::kMergeStride + col);
           if (f != 0.f) {
             a.x += f * v.x;
             a.y += f * v.y;
@@ -638,47 +735,29 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
             a.w += f * v.w;
           }
         }
-        out[it][4 * ps] = a.x;
-        out[it][4 * ps + 1] = a.y;
-        out[it][4 * ps + 2] = a.z;
-        out[it][4 * ps + 3] = a.w;
-      }
-    }
-#pragma unroll
-    for (int it = 0; it < RB; ++it) {
-      const int rloc = it * 16 + orow, r = row0 + rloc;
-      if (r >= p.R) continue;
-      if (whole) {
-        const int h = kh * p.g + r / p.Nq, i = r % p.Nq;
-        const float inv = lt[it] == 0.f ? 0.f : 1.f / lbt[it];
-        uint4* o = reinterpret_cast<uint4*>(p.o + 2 * (p.so.row(b, h, i) + ogrp * NT));
-#pragma unroll
-        for (int x = 0; x < NT; x += 8)
-          o[x / 8] = make_uint4(pack_bf16(out[it][x] * inv, out[it][x + 1] * inv),
-                                pack_bf16(out[it][x + 2] * inv, out[it][x + 3] * inv),
-                                pack_bf16(out[it][x + 4] * inv, out[it][x + 5] * inv),
-                                pack_bf16(out[it][x + 6] * inv, out[it][x + 7] * inv));
-        if (ogrp == 0)
-          p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] =
-              lt[it] == 0.f ? -INFINITY : (mt[it] + log2f(lt[it])) * 0.69314718055994531f;
-      } else {
-        const long long pr = static_cast<long long>(slot) * p.prow + rloc;
-        float4* o = reinterpret_cast<float4*>(p.part_o + pr * D + ogrp * NT);
-#pragma unroll
-        for (int x = 0; x < NT; x += 4)
-          o[x / 4] = make_float4(out[it][x], out[it][x + 1], out[it][x + 2], out[it][x + 3]);
-        if (ogrp == 0) p.part_m[pr] = make_float4(mt[it], lt[it], lbt[it], 0.f);
+        if (whole) {
+          const int hq = p.Nq == 1 ? r : r / p.Nq, h = kh * p.g + hq, i = r - hq * p.Nq;
+          const float inv = lt == 0.f ? 0.f : 1.f / lt, u = kQuant ? vt : 1.f;
+          *reinterpret_cast<uint2*>(p.o + 2 * (p.so.row(b, h, i) + col)) =
+              make_uint2(pack_bf16(a.x * inv * u, a.y * inv * u), pack_bf16(a.z * inv * u, a.w * inv * u));
+          if (col == 0)
+            p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] =
+                lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
+        } else {
+          const long long pr = static_cast<long long>(slot) * p.prow + rloc;
+          *reinterpret_cast<float4*>(p.part_o + pr * D + col) = a;
+          if (col == 0) p.part_m[pr] = make_float4(mt, lt, vt, 0.f);
+        }
       }
     }
     if (n == cnt - 1 && tid == 0) {
       int4 s = make_int4(0, 0, 0, 0);
       if (seg_starts_unit && !(flags & kFlagUnitEnd)) {  // goes on in the next CTAs
-        const long long end = t1 - (n - seg_first + 1) + paged_tiles(p, t.L);  // one past the unit's last tile
+        const long long end = t1 - (n - seg_first + 1) + paged_tiles(p, L);  // one past the unit's last tile
         s = make_int4(b, unit, static_cast<int>((end * G - 1) / W) - cta + 1, 0);
       }
       p.split[cta] = s;
     }
-    __syncthreads();  // merge and stat are free again
   }
   cp_async_wait<0>();
 }
@@ -686,7 +765,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_kernel(const PagedPara
 // Joins the partials of the units that several CTAs share: block (c, y) the
 // unit that starts in CTA c, 8 rows of it, a warp each.  Partial 0 is CTA c's
 // second slot, the others are the following CTAs' first.
-template <int D>
+template <int D, bool kQuant>
 __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(const PagedParams p, int rows_unit) {
   constexpr int E = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -700,30 +779,31 @@ __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(c
   auto at = [&](int i) {
     return (static_cast<long long>(2) * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.prow + rloc;
   };
-  float m = -INFINITY, l = 0.f, lb = 0.f, acc[E];
+  float m = -INFINITY, l = 0.f, u = 0x1p-126f, acc[E];  // u: the accumulators' unit, the largest so far
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int i0 = 0; i0 < parts; i0 += 32) {
-    float4 st = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    float4 st = make_float4(-INFINITY, 0.f, 0x1p-126f, 0.f);
     if (i0 + lane < parts) st = p.part_m[at(i0 + lane)];
-    float mn = fmaxf(m, st.x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    const float old = m == -INFINITY ? 0.f : exp2_fast(m - mn);
-    const float w = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : exp2_fast(st.x - mn);
-    m = mn;
-    l *= old;
-    lb *= old;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= old;
-    float ls = w == 0.f ? 0.f : w * st.y, lbs = w == 0.f ? 0.f : w * st.z;
+    float mn = fmaxf(m, st.x), un = fmaxf(u, st.z);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      ls += __shfl_xor_sync(0xffffffffu, ls, o);
-      lbs += __shfl_xor_sync(0xffffffffu, lbs, o);
+      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      un = fmaxf(un, __shfl_xor_sync(0xffffffffu, un, o));
     }
-    l += ls;
-    lb += lbs;
+    const float ui = __uint_as_float((254u << 23) - __float_as_uint(un));
+    float old = m == -INFINITY ? 0.f : exp2_fast(m - mn);
+    float w = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : exp2_fast(st.x - mn);
+    float ls = w == 0.f ? 0.f : w * st.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+    l = l * old + ls;
+    old *= u * ui;
+    w *= st.z * ui;
+    m = mn;
+    u = un;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= old;
     const int cnt = min(32, parts - i0);
 #pragma unroll 8
     for (int i = 0; i < cnt; ++i) {
@@ -747,10 +827,11 @@ __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(c
     }
   }
   const int h = kh * p.g + r / p.Nq, i = r % p.Nq;
-  const float inv = l == 0.f ? 0.f : 1.f / lb;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (!kQuant) u = 1.f;
   uint32_t* o = reinterpret_cast<uint32_t*>(p.o + 2 * (p.so.row(s.x, h, i) + lane * E));
 #pragma unroll
-  for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv * u, acc[e + 1] * inv * u);
   if (lane == 0)
     p.lse[(static_cast<long long>(s.x) * p.H + h) * p.Nq + i] =
         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
