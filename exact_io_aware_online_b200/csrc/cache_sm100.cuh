@@ -27,6 +27,8 @@ struct CacheParams {
   Strides pages, scales;  // elements; b = page, h = kv head, n = token
   long long table_stride;
   int B, Hkv, num_pages, page_size, max_pages;
+  uint32_t page_mul;  // ceil(2^(31 + page_shift) / page_size), page_shift = ceil(log2 page_size)
+  int page_shift;
 };
 
 constexpr float kE4m3Max = 448.f;
@@ -37,10 +39,16 @@ __device__ __forceinline__ int cache_length(const CacheParams& c, int b) {
   return static_cast<int>(max(0LL, min(static_cast<long long>(c.seqlens[b]), cap)));
 }
 
+// pos / page_size for 0 <= pos < 2^31: with e = page_mul * page_size - 2^(31 +
+// page_shift) < page_size <= 2^page_shift, pos * e / 2^(31 + page_shift) < 1.
+__device__ __forceinline__ int page_of(const CacheParams& c, int pos) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(pos)) * c.page_mul) >> (31 + c.page_shift));
+}
+
 // Page of position pos (0 <= pos < cache_length) of sequence b, or -1; *slot:
 // the token inside the page.
 __device__ __forceinline__ int cache_page(const CacheParams& c, int b, int pos, int* slot) {
-  const int i = pos / c.page_size;
+  const int i = page_of(c, pos);
   *slot = pos - i * c.page_size;
   const int page = c.table[b * c.table_stride + i];
   return page >= 0 && page < c.num_pages ? page : -1;

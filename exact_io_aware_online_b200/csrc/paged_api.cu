@@ -113,6 +113,9 @@ fa_status check_cache(const fa_paged_cache* c, fa_dtype dtype, bool written, fa:
   p->num_pages = c->num_pages;
   p->page_size = c->page_size;
   p->max_pages = c->max_pages;
+  p->page_shift = 0;
+  while ((1LL << p->page_shift) < c->page_size) ++p->page_shift;
+  p->page_mul = static_cast<uint32_t>(((1ULL << (31 + p->page_shift)) + c->page_size - 1) / c->page_size);
   return FA_OK;
 }
 
@@ -255,7 +258,7 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
   const long long cap = static_cast<long long>(cache->max_pages) * cache->page_size;
-  const double tiles = static_cast<double>((cap + fa::kPagedTile - 1) / fa::kPagedTile) * B * Hkv * p.nblk;
+  const double tiles = static_cast<double>((cap + 63) / 64) * B * Hkv * p.nblk;
   if (tiles / 148 > 1e9) return FA_ERR_UNSUPPORTED;  // a CTA counts its tiles in 32 bits
   const bool quant = cache->dtype == FA_CACHE_E4M3;
   if (d == 64) return quant ? launch_paged_rows<64, true>(p, tiles, st) : launch_paged_rows<64, false>(p, tiles, st);

@@ -15,9 +15,10 @@
 // filled by keys and by columns of V and only the rows are padded, to 8.
 //
 // Work: the keys that some row of a unit (sequence, kv head, block of rows) may
-// see are cut into tiles of 64.  All tiles of all units form one list, and CTA
-// c of G takes its c-th even share, whatever the lengths: it walks its tiles
-// through a cp.async ring that runs on from one unit into the next.  A unit
+// see are cut into tiles of 64 or 128.  All tiles of all units form one list,
+// and CTA c of G takes its c-th even share, whatever the lengths (beginning a
+// unit counts as much as a tile): it walks its tiles through a cp.async ring
+// that runs on from one unit into the next.  A unit
 // that lies in one share is finished by its CTA; one that several share leaves
 // a partial (m, l, accumulator) per CTA -- at most two per CTA, so the
 // workspace does not grow with the batch -- for paged_combine_kernel.
@@ -27,11 +28,11 @@
 
 namespace fa {
 
-constexpr int kPagedTile = 64;      // keys of a tile
 constexpr int kPagedThreads = 128;  // 4 warps
 constexpr int kPagedMaxCtas = 444;  // three on each of 148 SMs
 constexpr int kPagedCombineRows = 8;
 constexpr int kPagedRing = 8;       // descriptions of tiles: those staged, the one computed and the next one
+constexpr int kPagedOffs = 4;       // tiles' row offsets, from store() to issue()
 
 struct PagedParams {
   CacheParams c;
@@ -55,16 +56,17 @@ template <int D, bool kQuant, int NB, int RG>
 struct PagedCfg {
   static constexpr int kRows = 8 * NB * RG;  // rows of a unit
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
-  static constexpr int kTileBytes = kPagedTile * kRowBytes;
-  static constexpr int kScaleBytes = kQuant ? kPagedTile * 4 : 0;
+  static constexpr int kTile = kRowBytes == 256 ? 64 : 128;  // keys
+  static constexpr int kTileBytes = kTile * kRowBytes;
+  static constexpr int kScaleBytes = kQuant ? kTile * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + 2 * kScaleBytes;
   static constexpr int kCtas = kStageBytes >= 32768 || (D == 128 && NB == 2) ? 2 : 3;  // of an SM
-  static constexpr int kStages = kStageBytes >= 32768 || (kStageBytes >= 16384 && kCtas == 3) ? 3 : 5;
+  static constexpr int kStages = 3;
   static constexpr int kMergeStride = D + 4;  // floats; 2 * stride = 8 mod 32: a warp's stores meet every bank once
   static constexpr int kStatBytes = 4 * 8 * NB * 16;
-  static constexpr int kOffsBytes = kPagedRing * kPagedTile * 8;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kStatBytes + (kQuant ? 2 : 1) * kOffsBytes + kPagedRing * 32;
-  static_assert(kStages + 2 <= kPagedRing, "a tile's description outlives its copies");
+  static constexpr int kOffsBytes = kPagedOffs * kTile * 8;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kStatBytes + (kQuant ? 2 : 1) * kOffsBytes + kPagedRing * 48;
+  static_assert(kStages + 2 <= kPagedRing && kStages <= kPagedOffs, "a tile's description outlives its copies");
   static_assert(4 * 8 * kMergeStride * 4 <= kStageBytes, "the warps' accumulators are joined in a stage");
 };
 
@@ -122,10 +124,11 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t a) {
                : "r"(a)
                : "memory");
 }
-// Two e4m3 codes (the low one first) as two f16 numbers (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes (the lowest first) as f16 numbers (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t* lo, uint32_t* hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(x));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -157,14 +160,15 @@ __device__ __forceinline__ uint32_t v_at(int key, int chunk) {
 __device__ __forceinline__ int paged_first_key(const PagedParams& p, int L) {
   return p.window < 0 ? 0 : max(0, max(L - p.Nq, 0) - p.window);
 }
+template <int kTile>
 __device__ __forceinline__ int paged_tiles(const PagedParams& p, int L) {
-  return (L - paged_first_key(p, L) + kPagedTile - 1) / kPagedTile;
+  return (L - paged_first_key(p, L) + kTile - 1) / kTile;
 }
 
 struct PagedDesc {  // a tile, as the front of the pipeline describes it to the rest
   int b, unit, key0, flags, L;
-  uint32_t valid[2];  // keys that exist: in range and on a page
-  int pad;
+  uint32_t valid[4];  // keys that exist: in range and on a page
+  int pad[3];
 };
 constexpr int kFlagUnitStart = 1, kFlagUnitEnd = 2, kFlagSegEnd = 4;
 
@@ -175,34 +179,40 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   constexpr int KW = 4 / RG;                  // warps that share a tile's keys
   constexpr int DT = D / 16;                  // row tiles of O^T = V^T P^T
   constexpr int QS = D / 16;                  // k-steps of S^T = K Q^T
-  constexpr int ST = C::kStages, RB = C::kRowBytes;
+  constexpr int ST = C::kStages, RB = C::kRowBytes, TK = C::kTile;
+  constexpr int KS = TK / KW >= 32 ? 2 : 1;   // groups of 16 keys that a warp takes together
   constexpr int ES = kQuant ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   float4* stat = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);  // [4 warps][8 * NB rows]: m, l, unit
-  long long* offs = reinterpret_cast<long long*>(stat + 4 * 8 * NB);     // [ring][64] element offset of a row, -1: none
-  long long* soffs = offs + kPagedRing * kPagedTile;                     // [ring][64] offset of its scale
-  PagedDesc* desc = reinterpret_cast<PagedDesc*>(kQuant ? soffs + kPagedRing * kPagedTile : soffs);  // [ring]
+  long long* offs = reinterpret_cast<long long*>(stat + 4 * 8 * NB);     // [kPagedOffs][TK] byte offset of a row, -1: none
+  long long* soffs = offs + kPagedOffs * TK;                         // [kPagedOffs][TK] element offset of its scale
+  PagedDesc* desc = reinterpret_cast<PagedDesc*>(kQuant ? soffs + kPagedOffs * TK : soffs);  // [ring]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, B = p.c.B;
   const int U = p.c.Hkv * p.nblk;  // units of a sequence
 
-  // ---- this CTA's share [t0, t1) of the tile list
+  // ---- this CTA's share [s0, s1) of the list, in which a unit counts its tiles and c0
   long long* red = reinterpret_cast<long long*>(smem);
+  auto tiles_of = [&](int b) { return b < B ? paged_tiles<TK>(p, cache_length(p.c, b)) : 0; };
+  auto packed = [](int nt) { return (static_cast<long long>(nt) << 32) + (nt != 0); };  // tiles, sequences with keys
   long long sum = 0;
-  for (int b = tid; b < B; b += kPagedThreads) sum += paged_tiles(p, cache_length(p.c, b));
+  for (int b = tid; b < B; b += kPagedThreads) sum += packed(tiles_of(b));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) red[warp] = sum;
   __syncthreads();
-  const long long W = (red[0] + red[1] + red[2] + red[3]) * U;
-  const long long G = min(static_cast<long long>(gridDim.x), W);  // CTAs with a share: at least one tile each
-  const long long t0 = cta < G ? cta * W / G : 0, t1 = cta < G ? (cta + 1) * W / G : 0;
-  const int cnt = static_cast<int>(t1 - t0);
+  sum = red[0] + red[1] + red[2] + red[3];
+  const int c0 = (sum >> 32) * U >= 2LL * gridDim.x ? 1 : 0;  // few tiles: one for each CTA
+  auto cost = [&](long long x) { return ((x >> 32) + (x & 0xffffffffLL) * c0) * U; };
+  const long long W = cost(sum);
+  // CTAs with a share: c0 + 1 or more, so that each holds a tile
+  const long long G = min(static_cast<long long>(gridDim.x), W / (c0 + 1));
+  const long long s0 = cta < G ? cta * W / G : 0, s1 = cta < G ? (cta + 1) * W / G : 0;
 
   // rows of sequences without keys
   for (int b = cta; b < B; b += gridDim.x) {
-    if (paged_tiles(p, cache_length(p.c, b)) != 0) continue;
+    if (tiles_of(b) != 0) continue;
     for (long long r = tid; r < static_cast<long long>(p.H) * p.Nq; r += kPagedThreads) {
       const int h = static_cast<int>(r / p.Nq), i = static_cast<int>(r % p.Nq);
       uint4* o = reinterpret_cast<uint4*>(p.o + 2 * p.so.row(b, h, i));
@@ -211,19 +221,21 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       p.lse[static_cast<long long>(b) * p.H * p.Nq + r] = -INFINITY;
     }
   }
-  if (cnt == 0) {
+  if (cta >= G) {
     if (tid == 0) p.split[cta] = make_int4(0, 0, 0, 0);
     return;
   }
 
-  // ---- the front cursor: sequence, unit and tile of t0
-  int fb = 0, fu = 0, ft = 0, fL, fnt, fLnext;
+  // ---- the front cursor: sequence, unit and tile of s0; the tiles up to s1
+  int fb, fu, ft, fL, fnt, fLnext, cnt;
+  long long last_end;  // where the unit that s1 lies in ends
   {
     long long base = 0;
+    __syncthreads();
+    if (tid == 0) red[8] = (sum >> 32) * U, red[9] = W;  // s1 at the very end
     for (int at = 0;; at += kPagedThreads) {
-      const int b = at + tid;
-      const long long mine = b < B ? static_cast<long long>(paged_tiles(p, cache_length(p.c, b))) * U : 0;
-      long long incl = mine;
+      const int b = at + tid, nt = tiles_of(b);
+      long long incl = packed(nt);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -234,25 +246,41 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       __syncthreads();
       long long before = base;
       for (int w = 0; w < warp; ++w) before += red[w];
-      const long long lo = before + incl - mine, hi = before + incl;
-      if (lo <= t0 && t0 < hi) {
-        red[4] = b;
-        red[5] = t0 - lo;
+      const long long first = before + incl - packed(nt), lo = cost(first), hi = cost(before + incl);
+      if (nt != 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const long long at_s = e ? s1 : s0;
+          if (lo > at_s || at_s >= hi) continue;
+          const int u = static_cast<int>((at_s - lo) / (nt + c0)), off = static_cast<int>((at_s - lo) % (nt + c0));
+          const int t = max(0, off - c0);
+          const long long done = (first >> 32) * U + static_cast<long long>(u) * nt + t;  // tiles before it
+          if (e) {
+            red[8] = done;
+            red[9] = at_s - off + nt + c0;
+          } else {
+            red[4] = b;
+            red[5] = u;
+            red[6] = t;
+            red[7] = done;
+          }
+        }
       }
       base += red[0] + red[1] + red[2] + red[3];
-      if (t0 < base) break;  // found (uniform)
+      if (s1 < cost(base) || at + kPagedThreads >= B) break;  // found (uniform)
     }
     __syncthreads();
     fb = static_cast<int>(red[4]);
-    const long long off = red[5];
+    fu = static_cast<int>(red[5]);
+    ft = static_cast<int>(red[6]);
+    cnt = static_cast<int>(red[8] - red[7]);
+    last_end = red[9];
     __syncthreads();
     fL = cache_length(p.c, fb);
-    fnt = paged_tiles(p, fL);
-    fu = static_cast<int>(off / fnt);
-    ft = static_cast<int>(off % fnt);
+    fnt = paged_tiles<TK>(p, fL);
     fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
   }
-  const int frow = tid & (kPagedTile - 1);
+  const int frow = tid & (TK - 1);
   struct Tile {  // a tile as fetch() leaves it for store(): this thread's row
     int page, slot, b, u, key0, flags, L;
   };
@@ -264,12 +292,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     t.b = fb;
     t.u = fu;
     t.L = fL;
-    t.key0 = paged_first_key(p, fL) + ft * kPagedTile;
+    t.key0 = paged_first_key(p, fL) + ft * TK;
     t.flags = (ft == 0 ? kFlagUnitStart : 0) | (ft == fnt - 1 ? kFlagUnitEnd | kFlagSegEnd : 0) |
               (n == cnt - 1 ? kFlagSegEnd : 0);
     const int pos = t.key0 + frow;
-    if (pos < fL) {
-      const int i = pos / p.c.page_size;
+    if (tid < TK && pos < fL) {
+      const int i = page_of(p.c, pos);
       t.slot = pos - i * p.c.page_size;
       t.page = p.c.table[fb * p.c.table_stride + i];
     }
@@ -282,7 +310,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
             ++fb;
             fL = fLnext;
             fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
-            fnt = paged_tiles(p, fL);
+            fnt = paged_tiles<TK>(p, fL);
           } while (fnt == 0 && fb < B - 1);
         }
       }
@@ -294,8 +322,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     if (n >= cnt) return;
     const bool on = f.page >= 0 && f.page < p.c.num_pages;
     const int kh = p.nblk == 1 ? f.u : f.u / p.nblk;
-    if (tid < kPagedTile) {
-      offs[(n % kPagedRing) * kPagedTile + frow] = on ? p.c.pages.row(f.page, kh, f.slot) * ES : -1;
+    if (tid < TK) {
+      offs[(n % kPagedOffs) * TK + tid] = on ? p.c.pages.row(f.page, kh, f.slot) * ES : -1;
+      if (kQuant) soffs[(n % kPagedOffs) * TK + tid] = on ? p.c.scales.row(f.page, kh, f.slot) : -1;
       const uint32_t m = __ballot_sync(0xffffffffu, on);
       PagedDesc& t = desc[n % kPagedRing];
       if (lane == 0) t.valid[warp] = m;
@@ -306,8 +335,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
         t.flags = f.flags;
         t.L = f.L;
       }
-    } else if (kQuant) {
-      soffs[(n % kPagedRing) * kPagedTile + frow] = on ? p.c.scales.row(f.page, kh, f.slot) : -1;
     }
   };
   const uint32_t smem0 = paged_smem(smem);
@@ -317,9 +344,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   auto issue = [&](int n) {
     if (n < cnt) {
       const uint32_t dst = smem0 + (n % ST) * C::kStageBytes;
-      const long long* src = offs + (n % kPagedRing) * kPagedTile + crow;
+      const long long* src = offs + (n % kPagedOffs) * TK + crow;
 #pragma unroll
-      for (int i = 0; i < kPagedTile / RPI; ++i) {
+      for (int i = 0; i < TK / RPI; ++i) {
         const int row = crow + i * RPI;
         const long long off = src[i * RPI];
         const bool on = off >= 0;
@@ -328,9 +355,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
         cp_async16(dst + C::kTileBytes + v_at<RB, kQuant>(row, chunk), p.c.v + at, on);
       }
       if (kQuant) {
-        const long long off = soffs[(n % kPagedRing) * kPagedTile + frow];
-        const float* src = (tid < kPagedTile ? p.c.ks : p.c.vs) + (off >= 0 ? off : 0);
-        cp_async4(dst + 2 * C::kTileBytes + tid * 4, src, off >= 0);
+        const long long off = soffs[(n % kPagedOffs) * TK + tid], at = off >= 0 ? off : 0;
+        cp_async4(dst + 2 * C::kTileBytes + tid * 4, p.c.ks + at, off >= 0);
+        cp_async4(dst + 2 * C::kTileBytes + (TK + tid) * 4, p.c.vs + at, off >= 0);
       }
     }
     cp_async_commit();
@@ -344,7 +371,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   int rlo[NB][2], rhi[NB][2];  // keys that the thread's rows may see
   int free_lo = 0, free_hi = 0;  // keys that every row of the unit may see
   bool seg_starts_unit = false, fresh = true;  // fresh: the next tile begins a segment
-  int seg_first = 0;
   auto dcol = [&](int x, int e) { return kQuant ? rq * (D / 8) + 2 * x + e : 16 * x + 8 * e + rq; };
   // the queries of unit t, as they are in memory
   auto load_q = [&](const PagedDesc& t) {
@@ -396,7 +422,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     if (fresh) {
       fresh = false;
       seg_starts_unit = flags & kFlagUnitStart;
-      seg_first = n;
       const int L = t.L, row0 = (p.nblk == 1 ? 0 : t.unit % p.nblk * C::kRows) + rg * 8 * NB;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -446,99 +471,116 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 
     const uint32_t sK = smem0 + (n % ST) * C::kStageBytes, sV = sK + C::kTileBytes;
     const float* scl = reinterpret_cast<const float*>(smem + (n % ST) * C::kStageBytes + 2 * C::kTileBytes);
-    const bool edge = key0 < free_lo || key0 + kPagedTile > free_hi || (t.valid[0] & t.valid[1]) != 0xffffffffu;
+    bool edge = key0 < free_lo || key0 + TK > free_hi;
+#pragma unroll
+    for (int i = 0; i < TK / 32; ++i) edge |= t.valid[i] != 0xffffffffu;
 #pragma unroll 1
-    for (int s = 0; s < RG; ++s) {
-      const int kb = (kw * RG + s) * 16;
-      // ---- S^T of keys kb + rq (elements 0, 1) and kb + rq + 8 (2, 3), rows 2 qd and 2 qd + 1
-      float sc[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
-      if (kQuant) {
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const uint4 a = lds128(sK + k_at<RB>(kb + rq, qd + 4 * i)), b = lds128(sK + k_at<RB>(kb + rq + 8, qd + 4 * i));
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t a0 = e4m3x2_to_f16x2(aw[x] & 0xffffu), a2 = e4m3x2_to_f16x2(aw[x] >> 16),
-                           a1 = e4m3x2_to_f16x2(bw[x] & 0xffffu), a3 = e4m3x2_to_f16x2(bw[x] >> 16);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[nb], a0, a1, a2, a3, qb[nb][i * 4 + x]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 a = lds128(sK + k_at<RB>(kb + rq, qd + 4 * i)), b = lds128(sK + k_at<RB>(kb + rq + 8, qd + 4 * i));
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma16<false>(sc[nb], a.x, b.x, a.y, b.y, qb[nb][2 * i]);
-            mma16<false>(sc[nb], a.z, b.z, a.w, b.w, qb[nb][2 * i + 1]);
-          }
-        }
-      }
-      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
-      if (kQuant) {
-        ks[0] = scl[kb + rq];
-        ks[1] = scl[kb + rq + 8];
-        vs[0] = scl[kPagedTile + kb + rq];
-        vs[1] = scl[kPagedTile + kb + rq + 8];
-      }
-      uint32_t allowed = 0xffffffffu;  // bit 4 nb + e
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[nb][e] *= rowf[nb][e & 1];
-          if (kQuant) sc[nb][e] *= ks[e >> 1];
-        }
+    for (int s = 0; s < TK / KW / (16 * KS); ++s) {
+      const int kb = (kw * (TK / KW / (16 * KS)) + s) * 16 * KS;
+      uint32_t vm = 0xffffffffu;
       if (edge) {
-        const uint32_t vm = t.valid[kb >> 5] >> (kb & 31);
+        vm = t.valid[kb >> 5] >> (kb & 31);
+        if ((KS == 2 ? vm : vm & 0xffffu) == 0) continue;  // behind the end
+      }
+      // ---- S^T of keys 16 k + rq (elements 0, 1) and 16 k + rq + 8 (2, 3), rows 2 qd and 2 qd + 1
+      float sc[KS][NB][4];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[k][nb][0] = sc[k][nb][1] = sc[k][nb][2] = sc[k][nb][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < (kQuant ? D / 64 : D / 32); ++i)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint4 a = lds128(sK + k_at<RB>(kb + 16 * k + rq, qd + 4 * i)),
+                      b = lds128(sK + k_at<RB>(kb + 16 * k + rq + 8, qd + 4 * i));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+          if (kQuant) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(aw[x], &a0, &a2);
+              e4m3x4_to_f16(bw[x], &a1, &a3);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[k][nb], a0, a1, a2, a3, qb[nb][(i * 4 + x) % QS]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16<false>(sc[k][nb], aw[2 * x], bw[2 * x], aw[2 * x + 1], bw[2 * x + 1], qb[nb][(2 * i + x) % QS]);
+          }
+        }
+      float vs[KS][2];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float ks = kQuant ? scl[kb + 16 * k + 8 * h + rq] : 1.f;
+          vs[k][h] = kQuant ? scl[TK + kb + 16 * k + 8 * h + rq] : 1.f;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              sc[k][nb][2 * h + c] *= rowf[nb][c];
+              if (kQuant) sc[k][nb][2 * h + c] *= ks;
+            }
+        }
+      uint32_t allowed = 0xffffffffu;  // bit 4 (k NB + nb) + e
+      if (edge) {
         allowed = 0;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = rq + 8 * (e >> 1), j = key0 + kb + k;
-            if (((vm >> k) & 1) && j >= rlo[nb][e & 1] && j < rhi[nb][e & 1])
-              allowed |= 1u << (4 * nb + e);
-            else
-              sc[nb][e] = -INFINITY;
-          }
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = 16 * k + rq + 8 * (e >> 1), j = key0 + kb + key;
+              if (((vm >> key) & 1) && j >= rlo[nb][e & 1] && j < rhi[nb][e & 1])
+                allowed |= 1u << (4 * (k * NB + nb) + e);
+              else
+                sc[k][nb][e] = -INFINITY;
+            }
       }
+      auto on = [&](int k, int nb, int e) { return ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
       // ---- running maximum: moved only when it grows by more than 8 (weights
       // stay below 2^8).  Quantised: weights reach the second product as f16
       // multiples of the largest value scale so far (vref, a power of two above
       // it); a row's accumulator counts in units of its vref.
       bool grow = false;
+      float mx[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          grow |= fmaxf(sc[nb][c], sc[nb][2 + c]) > m[nb][c] + 8.f;
+          mx[nb][c] = fmaxf(sc[0][nb][c], sc[0][nb][2 + c]);
+          if (KS == 2) mx[nb][c] = fmaxf(mx[nb][c], fmaxf(sc[KS - 1][nb][c], sc[KS - 1][nb][2 + c]));
+          grow |= mx[nb][c] > m[nb][c] + 8.f;
           if (kQuant)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              grow |= fabsf(vs[h]) >= vref[nb][c] && ((allowed >> (4 * nb + 2 * h + c)) & 1);
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) grow |= fabsf(vs[k][h]) >= vref[nb][c] && on(k, nb, 2 * h + c);
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(sc[nb][c], sc[nb][2 + c]);
             uint32_t ve = 0;
             if (kQuant)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if ((allowed >> (4 * nb + 2 * h + c)) & 1) ve = max(ve, (__float_as_uint(vs[h]) >> 23) & 0xffu);
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (on(k, nb, 2 * h + c)) ve = max(ve, (__float_as_uint(vs[k][h]) >> 23) & 0xffu);
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) {
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              mx[nb][c] = fmaxf(mx[nb][c], __shfl_xor_sync(0xffffffffu, mx[nb][c], o));
               if (kQuant) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, o));
             }
-            const float mn = mx > m[nb][c] + 8.f ? mx : m[nb][c];
+            const float mn = mx[nb][c] > m[nb][c] + 8.f ? mx[nb][c] : m[nb][c];
             float f = m[nb][c] == mn ? 1.f : exp2_fast(m[nb][c] - mn);
             m[nb][c] = mn;
             l[nb][c] *= f;
@@ -557,126 +599,133 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       }
       // The weights are rounded to 16 bits for the second product: bf16 (half a
       // step is 2^-8 of a weight), or f16 of weight * value scale / vref, 2^-11
-      // of it down to 2^-14; rows that hold a scale below 2^-12 vref take the
-      // slow form below.
-      uint32_t pb[NB][2];
-      bool slow = false;
+      // of it down to 2^-14; keys whose scale is below 2^-12 vref take the slow
+      // form below.
+      uint32_t pb[KS][NB][2];
+      bool slow[KS];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float mu = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
-          const float w = exp2_fast(sc[nb][e] - mu);
-          l[nb][e & 1] += w;
-          sc[nb][e] = w;
-          if (kQuant) {
-            const float u = vs[e >> 1] * vinv[nb][e & 1];
-            const bool on = (allowed >> (4 * nb + e)) & 1;
-            slow |= on && fabsf(u) < 0x1p-12f && fabsf(vs[e >> 1]) > 0x1p-90f;
-            sc[nb][e] = on ? w * u : 0.f;
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          pb[nb][h] = transpose8x8(kQuant ? pack_f16(sc[nb][2 * h], sc[nb][2 * h + 1])
-                                          : pack_bf16(sc[nb][2 * h], sc[nb][2 * h + 1]));
-      }
-      // ---- O^T += V^T P^T
-      uint32_t bad = slow;
-      if (kQuant) {
-        uint32_t w[4][D / 32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = kb + 2 * qd + (k & 1) + 8 * (k >> 1);
-          if (D == 128) {
-            const uint4 v = lds128(sV + v_at<RB, kQuant>(key, rq));
-            w[k][0] = v.x;
-            w[k][1] = v.y;
-            w[k][2 % (D / 32)] = v.z;
-            w[k][3 % (D / 32)] = v.w;
-          } else {
-            const uint2 v = lds64(sV + v_at<RB, kQuant>(key, rq >> 1) + (rq & 1) * 8);
-            w[k][0] = v.x;
-            w[k][1] = v.y;
-          }
-        }
-        if (edge)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) bad |= ((w[k][y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // NaN codes
-        if (!__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-          for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
-            const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
-            const uint32_t lo = __byte_perm(w[0][x >> 1], w[1][x >> 1], sel), hi = __byte_perm(w[2][x >> 1], w[3][x >> 1], sel);
-            const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xffffu), a1 = e4m3x2_to_f16x2(lo >> 16),
-                           a2 = e4m3x2_to_f16x2(hi & 0xffffu), a3 = e4m3x2_to_f16x2(hi >> 16);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[nb]);
-          }
-          continue;
-        }
-      } else {
-        const int key = kb + (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t at = sV + v_at<RB, kQuant>(key, (lane >> 3) & 1);
-        if (edge) {
-#pragma unroll
-          for (int x = 0; x < DT; ++x) {
-            uint32_t a[4];
-            ldmatrix_x4_trans(a, at ^ (x << 5));
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              bad |= ((a[y] & 0x7f80u) == 0x7f80u) | ((a[y] & 0x7f800000u) == 0x7f800000u);
-          }
-        }
-        if (!edge || !__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-          for (int x = 0; x < DT; ++x) {
-            uint32_t a[4];
-            ldmatrix_x4_trans(a, at ^ (x << 5));
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x], a[0], a[1], a[2], a[3], pb[nb]);
-          }
-          continue;
-        }
-      }
-      // The slow form: products one by one in fp32, weights of zero left out.
-      // For an infinity or NaN among the values of a tile that some rows see
-      // only in part (0 * infinity would reach rows that may not see that key),
-      // and for value scales too far apart for f16.
-#pragma unroll 1
-      for (int k = 0; k < 16; ++k)
+      for (int k = 0; k < KS; ++k) {
+        slow[k] = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const int src = (k & 7) * 4 + qd;
-          const float f0 = __shfl_sync(0xffffffffu, k < 8 ? sc[nb][0] : sc[nb][2], src);
-          const float f1 = __shfl_sync(0xffffffffu, k < 8 ? sc[nb][1] : sc[nb][3], src);
 #pragma unroll
-          for (int x = 0; x < DT; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int col = dcol(x, e);
-              const uint32_t at = sV + v_at<RB, kQuant>(kb + k, col * ES / 16) + (col * ES) % 16;
-              uint32_t z;
-              float v;
-              if (kQuant) {
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
-                v = e4m3x2_to_float2(static_cast<uint16_t>(z)).x;
-              } else {
-                asm volatile("ld.shared.u16 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
-                v = __uint_as_float(z << 16);
-              }
-              if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
-              if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
+          for (int e = 0; e < 4; ++e) {
+            const float mu = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
+            const float w = exp2_fast(sc[k][nb][e] - mu);
+            l[nb][e & 1] += w;
+            sc[k][nb][e] = w;
+            if (kQuant) {
+              const float u = vs[k][e >> 1] * vinv[nb][e & 1];
+              slow[k] |= on(k, nb, e) && fabsf(u) < 0x1p-12f && fabsf(vs[k][e >> 1]) > 0x1p-90f;
+              sc[k][nb][e] = on(k, nb, e) ? w * u : 0.f;
             }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            pb[k][nb][h] = transpose8x8(kQuant ? pack_f16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1])
+                                               : pack_bf16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1]));
         }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int kk = kb + 16 * k;
+        uint32_t bad = slow[k];
+        if (kQuant) {
+          uint32_t w[4][D / 32];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int key = kk + 2 * qd + (y & 1) + 8 * (y >> 1);
+            if (D == 128) {
+              const uint4 v = lds128(sV + v_at<RB, kQuant>(key, rq));
+              w[y][0] = v.x;
+              w[y][1] = v.y;
+              w[y][2 % (D / 32)] = v.z;
+              w[y][3 % (D / 32)] = v.w;
+            } else {
+              const uint2 v = lds64(sV + v_at<RB, kQuant>(key, rq >> 1) + (rq & 1) * 8);
+              w[y][0] = v.x;
+              w[y][1] = v.y;
+            }
+          }
+          if (edge)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int z = 0; z < D / 32; ++z) bad |= ((w[y][z] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // NaN codes
+          if (!__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
+              const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(__byte_perm(w[0][x >> 1], w[1][x >> 1], sel), &a0, &a1);
+              e4m3x4_to_f16(__byte_perm(w[2][x >> 1], w[3][x >> 1], sel), &a2, &a3);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[k][nb]);
+            }
+            continue;
+          }
+        } else {
+          const int key = kk + (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t at = sV + v_at<RB, kQuant>(key, (lane >> 3) & 1);
+          if (edge) {
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {
+              uint32_t a[4];
+              ldmatrix_x4_trans(a, at ^ (x << 5));
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                bad |= ((a[y] & 0x7f80u) == 0x7f80u) | ((a[y] & 0x7f800000u) == 0x7f800000u);
+            }
+          }
+          if (!edge || !__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {
+              uint32_t a[4];
+              ldmatrix_x4_trans(a, at ^ (x << 5));
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x], a[0], a[1], a[2], a[3], pb[k][nb]);
+            }
+            continue;
+          }
+        }
+        // The slow form: products one by one in fp32, weights of zero left out.
+        // For an infinity or NaN among the values of a tile that some rows see
+        // only in part (0 * infinity would reach rows that may not see that key),
+        // and for value scales too far apart for f16.
+#pragma unroll 1
+        for (int y = 0; y < 16; ++y)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int src = (y & 7) * 4 + qd;
+            const float f0 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][0] : sc[k][nb][2], src);
+            const float f1 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][1] : sc[k][nb][3], src);
+#pragma unroll
+            for (int x = 0; x < DT; ++x)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = dcol(x, e);
+                const uint32_t at = sV + v_at<RB, kQuant>(kk + y, col * ES / 16) + (col * ES) % 16;
+                uint32_t z;
+                float v;
+                if (kQuant) {
+                  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
+                  v = e4m3x2_to_float2(static_cast<uint16_t>(z)).x;
+                } else {
+                  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
+                  v = __uint_as_float(z << 16);
+                }
+                if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
+                if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
+              }
+          }
+      }
     }
 
     if (!(flags & kFlagSegEnd)) continue;
     // ---- the segment's end: the KW warps of a row group join their states in tile n's stage
     fresh = true;
-    const int b = t.b, unit = t.unit, L = t.L;
+    const int b = t.b, unit = t.unit;
     const int kh = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - kh * p.nblk) * C::kRows;
     const bool whole = seg_starts_unit && (flags & kFlagUnitEnd);
     const int slot = 2 * cta + (seg_starts_unit ? 1 : 0);
@@ -753,8 +802,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     if (n == cnt - 1 && tid == 0) {
       int4 s = make_int4(0, 0, 0, 0);
       if (seg_starts_unit && !(flags & kFlagUnitEnd)) {  // goes on in the next CTAs
-        const long long end = t1 - (n - seg_first + 1) + paged_tiles(p, L);  // one past the unit's last tile
-        s = make_int4(b, unit, static_cast<int>((end * G - 1) / W) - cta + 1, 0);
+        s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - cta + 1, 0);
       }
       p.split[cta] = s;
     }
