@@ -125,7 +125,7 @@ def _dtype_code(t) -> int:
 
 def _stream_ptr(device) -> int:
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream(device).cuda_stream without the objects
 
 
 def _check(code: int, what: str):
@@ -138,6 +138,8 @@ def _on(device, fn, *args):
     the stream it is given and rejects a stream of another device than the
     current one."""
     import torch
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
 
@@ -589,72 +591,78 @@ class _PagedCache(ctypes.Structure):
 
 def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
     """Checks a paged cache's tensors against each other; the _PagedCache that
-    describes them (it holds pointers only: the tensors stay the caller's)."""
+    describes them (it holds pointers only: the tensors stay the caller's) and
+    their device."""
     import torch
     if k_pages.dim() != 4:
         raise ValueError("k_pages, v_pages must be 4-D [pages, kv heads, page size, head_dim]")
-    if k_pages.dtype == torch.bfloat16:
+    dtype = k_pages.dtype
+    if dtype == torch.bfloat16:
         code = FA_CACHE_BF16
-    elif k_pages.dtype == torch.float8_e4m3fn:
+    elif dtype == torch.float8_e4m3fn:
         code = FA_CACHE_E4M3
     else:
-        raise TypeError(f"k_pages: unsupported dtype {k_pages.dtype} (bfloat16 or float8_e4m3fn)")
-    device, shape, st = k_pages.device, k_pages.shape, k_pages.stride()
+        raise TypeError(f"k_pages: unsupported dtype {dtype} (bfloat16 or float8_e4m3fn)")
+    shape, st = k_pages.shape, k_pages.stride()
     if v_pages.shape != shape:
         raise ValueError(f"v_pages: shape {tuple(v_pages.shape)}, expected {tuple(shape)}")
-    if v_pages.dtype != k_pages.dtype:
-        raise TypeError(f"v_pages: dtype {v_pages.dtype}, expected {k_pages.dtype}")
+    if v_pages.dtype != dtype:
+        raise TypeError(f"v_pages: dtype {v_pages.dtype}, expected {dtype}")
     if v_pages.stride() != st or st[3] != 1:
         raise ValueError("k_pages, v_pages must have the same strides and a contiguous last axis")
     P, Hkv, page, d = shape
-    if page_table.dim() != 2 or seqlens.dim() != 1 or page_table.shape[0] != seqlens.shape[0]:
+    table_shape, table_stride = page_table.shape, page_table.stride()
+    if len(table_shape) != 2 or seqlens.shape != table_shape[:1]:
         raise ValueError("page_table must be [sequences, pages of a sequence] and seqlens [sequences]")
     if page_table.dtype != torch.int32 or seqlens.dtype != torch.int32:
         raise TypeError("page_table and seqlens must be int32")
-    B, M = page_table.shape
-    if (M > 1 and page_table.stride(1) != 1) or (B > 1 and (page_table.stride(0) < M or seqlens.stride(0) != 1)):
+    B, M = table_shape
+    if (M > 1 and table_stride[1] != 1) or (B > 1 and (table_stride[0] < M or seqlens.stride(0) != 1)):
         raise ValueError("page_table must have contiguous rows that do not overlap, and seqlens must be contiguous")
+    tensors = [(v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens")]
+    ks = vs = ss = None
     if code == FA_CACHE_BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale, v_scale belong to a float8_e4m3fn cache")
-        scales = _Strides(0, 0, 0)
-        tensors = ((v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens"))
     else:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is None or t.shape != shape[:3] or t.dtype != torch.float32:
                 raise ValueError(f"{name}: must be a float32 tensor of shape {tuple(shape[:3])}")
-        if k_scale.stride() != v_scale.stride():
+        ss = k_scale.stride()
+        if v_scale.stride() != ss:
             raise ValueError("k_scale, v_scale must have the same strides")
-        scales = _Strides(*k_scale.stride())
-        tensors = ((v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens"), (k_scale, "k_scale"),
-                   (v_scale, "v_scale"))
+        tensors += [(k_scale, "k_scale"), (v_scale, "v_scale")]
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     if not k_pages.is_cuda:
-        raise ValueError(f"k_pages: must be on a CUDA device, got {device}")
+        raise ValueError(f"k_pages: must be on a CUDA device, got {k_pages.device}")
+    at = k_pages.get_device()
     for t, name in tensors:
-        if t.device != device:
-            raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {device})")
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr() if code else None,
-                       v_scale.data_ptr() if code else None, page_table.data_ptr(), seqlens.data_ptr(),
-                       _Strides(st[0], st[1], st[2]), scales, page_table.stride(0), B, Hkv, d, P, page, M, code)
+        if t.get_device() != at:
+            raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {k_pages.device})")
+    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, page_table.data_ptr(), seqlens.data_ptr(),
+                       st[:3], ss or (0, 0, 0), table_stride[0], B, Hkv, d, P, page, M, code), k_pages.device
 
 
 def _move_args(c, k, v, cu_seqlens, T, device):
     """Checks the packed tokens k, v [T, Hkv, d] (d contiguous) and the device
     offsets of cache_write() / cache_read(); their fa_strides."""
     import torch
+    shape, at, strides = (T, c.Hkv, c.d), device.index, []
     for t, name in ((k, "k"), (v, "v")):
-        if t.dim() != 3 or tuple(t.shape) != (T, c.Hkv, c.d):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, c.Hkv, c.d)}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
-        if t.stride(2) != 1:
+        st = t.stride()
+        if st[2] != 1:
             raise ValueError(f"{name}: must have a contiguous last axis")
-        if t.device != device:
+        if t.get_device() != at:
             raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {device})")
-    if cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (c.B + 1,) or cu_seqlens.device != device \
+        strides.append((1, st[1], st[0]))
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (c.B + 1,) or cu_seqlens.get_device() != at \
             or cu_seqlens.stride(0) != 1:
         raise TypeError(f"cu_seqlens must be a contiguous int32 tensor of {c.B + 1} values on the device of k_pages")
-    return (_Strides * 2)(_Strides(1, k.stride(1), k.stride(0)), _Strides(1, v.stride(1), v.stride(0)))
+    return (_Strides * 2)(*strides)
 
 
 def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale=None, v_scale=None):
@@ -665,8 +673,8 @@ def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale
     scale per token and kv head in k_scale, v_scale [P,Hkv,page] float32,
     float8_e4m3fn; page_table [B,pages of a sequence], cu_seqlens and seqlens
     int32, all on one CUDA device."""
-    c = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
-    T, device = k.shape[0], k_pages.device
+    c, device = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    T = k.shape[0]
     st = _move_args(c, k, v, cu_seqlens, T, device)
     if T == 0:
         return
@@ -683,11 +691,11 @@ def cache_read(k_pages, v_pages, page_table, cu_seqlens, seqlens, num_tokens: in
     any token and head strides; its rows outside the offsets are left as they
     were (uninitialised when allocated here)."""
     import torch
-    c = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
-    T, device = int(num_tokens), k_pages.device
+    c, device = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    T = int(num_tokens)
     if out is None:
         k = torch.empty((T, c.Hkv, c.d), dtype=torch.bfloat16, device=device)
-        v = torch.empty((T, c.Hkv, c.d), dtype=torch.bfloat16, device=device)
+        v = torch.empty_like(k)
     else:
         k, v = out
     st = _move_args(c, k, v, cu_seqlens, T, device)
@@ -710,8 +718,7 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
     values already: fwd_decode() for sequences of different lengths (see
     fa_fwd_paged in fa.h; the cache's tensors are those of cache_write())."""
     import torch
-    c = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
-    device = k_pages.device
+    c, device = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
     if q.dim() != 4:
         raise ValueError("q must be 4-D [batch, heads, rows, head_dim]")
     B, H, Nq, d = q.shape
@@ -719,7 +726,7 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
         raise ValueError(f"q: shape {tuple(q.shape)}, expected {c.B} sequences of head_dim {c.d}")
     if q.dtype != torch.bfloat16:
         raise TypeError(f"q: dtype {q.dtype}, expected torch.bfloat16")
-    if q.device != device:
+    if q.get_device() != device.index:
         raise ValueError(f"q: must be on the CUDA device of k_pages, got {q.device} (k_pages: {device})")
     if out is not None:
         _same(out, q.shape, q, "out", contiguous=False)
@@ -727,14 +734,15 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
         _check_lse(lse, (B, H, Nq), q)
     if workspace is not None:
         _check_workspace(workspace, device)
-    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=device) if out is None else out
+    dense = q.is_contiguous()
+    o = (torch.empty_like(q) if dense else q.new_empty((B, H, Nq, d))) if out is None else out
     l = torch.empty((B, H, Nq), dtype=torch.float32, device=device) if lse is None else lse
-    st = _strides_of(q, o)
+    st = None if dense and (out is None or out.is_contiguous()) else _strides_of(q, o)
     ws = torch.empty(max(fwd_paged_workspace_size(B, H, c.Hkv, Nq, d), 16), dtype=torch.uint8, device=device) \
         if workspace is None else workspace
     code = _on(device, lib().fa_fwd_paged, ctypes.addressof(c), q.data_ptr(), o.data_ptr(), l.data_ptr(),
-               ctypes.addressof(st), H, Nq, 1.0 / math.sqrt(d) if scale is None else float(scale), int(bool(causal)),
-               int(window), ws.data_ptr(), ws.numel(), FA_BF16, _stream_ptr(device))
+               None if st is None else ctypes.addressof(st), H, Nq, 1.0 / math.sqrt(d) if scale is None else float(scale),
+               int(bool(causal)), int(window), ws.data_ptr(), ws.numel(), FA_BF16, _stream_ptr(device))
     _check(code, "fa_fwd_paged")
     return o, l
 

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <utility>
@@ -172,13 +173,24 @@ PagedOffsets paged_offsets(int rows, int d) {
 int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // rows of a unit
 
 template <int D, bool kQuant, int NB, int RG>
-fa_status launch_paged(const fa::PagedParams& p, double tiles, cudaStream_t st) {
+fa_status launch_paged(fa::PagedParams p, double tiles, cudaStream_t st) {
   using C = fa::PagedCfg<D, kQuant, NB, RG>;
   const auto kernel = fa::paged_kernel<D, kQuant, NB, RG>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-    return FA_ERR_CUDA;
-  // no more CTAs than the lengths could give tiles
-  const int ctas = static_cast<int>(std::min<double>(148 * C::kCtas, tiles));
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};  // devices on which this kernel may use its shared memory
+  const uint64_t bit = dev < 64 ? 1ULL << dev : 0;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+      return FA_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  // lanes: the largest divisor of a sequence's units that leaves at most one CTA in sixteen without work
+  const int units = p.c.Hkv * p.nblk, most = 148 * C::kCtas;
+  p.lanes = std::min(units, most);
+  while (units % p.lanes != 0 || most % p.lanes > most / 16) --p.lanes;
+  // no more groups than the lengths could give tiles
+  const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles));
   const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, p);
   if (s != FA_OK) return s;
   const dim3 grid(ctas, (p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
@@ -258,7 +270,7 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
   const long long cap = static_cast<long long>(cache->max_pages) * cache->page_size;
-  const double tiles = static_cast<double>((cap + 63) / 64) * B * Hkv * p.nblk;
+  const double tiles = static_cast<double>((cap + 63) / 64) * B * Hkv * p.nblk;  // at most
   if (tiles / 148 > 1e9) return FA_ERR_UNSUPPORTED;  // a CTA counts its tiles in 32 bits
   const bool quant = cache->dtype == FA_CACHE_E4M3;
   if (d == 64) return quant ? launch_paged_rows<64, true>(p, tiles, st) : launch_paged_rows<64, false>(p, tiles, st);

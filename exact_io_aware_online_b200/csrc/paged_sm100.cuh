@@ -15,13 +15,17 @@
 // filled by keys and by columns of V and only the rows are padded, to 8.
 //
 // Work: the keys that some row of a unit (sequence, kv head, block of rows) may
-// see are cut into tiles of 64 or 128.  All tiles of all units form one list,
-// and CTA c of G takes its c-th even share, whatever the lengths (beginning a
-// unit counts as much as a tile): it walks its tiles through a cp.async ring
-// that runs on from one unit into the next.  A unit
-// that lies in one share is finished by its CTA; one that several share leaves
-// a partial (m, l, accumulator) per CTA -- at most two per CTA, so the
-// workspace does not grow with the batch -- for paged_combine_kernel.
+// see are cut into tiles of 64 or 128.  The CTAs form groups of `lanes`, a lane
+// for each unit of a sequence (or every lanes-th), so that a group reads the
+// same tokens' heads at the same time: heads inside tokens are then whole DRAM
+// rows, the 32-byte sectors of the scales are read from DRAM once, and blocks
+// of rows share their keys in L2.  The tiles of all sequences form one list, and
+// group c of G takes its c-th even share, whatever the lengths (beginning a
+// unit counts as much as a tile): each CTA walks its tiles through a cp.async
+// ring that runs on from one unit into the next.  A unit that lies in one share
+// is finished by its CTA; one that several share leaves a partial (m, l,
+// accumulator) per CTA -- at most two per CTA, so the workspace does not grow
+// with the batch -- for paged_combine_kernel.
 #pragma once
 
 #include "cache_sm100.cuh"
@@ -44,10 +48,11 @@ struct PagedParams {
   float scale_log2;
   int causal, window;
   int R, nblk;     // rows of a kv head (g * Nq), units they make
+  int lanes;       // CTAs of a group: a divisor of Hkv * nblk
   int prow;        // rows of a partial: min(R, rows of a unit)
   float* part_o;   // [2 * G][prow][D]
   float4* part_m;  // [2 * G][prow]: m, l, unit of the accumulator
-  int4* split;     // [G]: the unit that starts in CTA c and goes on in later ones: b, unit, CTAs it spans (or 0)
+  int4* split;     // [CTAs]: the unit that starts in CTA c and goes on in its lane: b, unit, CTAs it spans (or 0)
 };
 
 // A warp holds NB blocks of 8 rows; RG groups of warps hold different rows, the
@@ -190,9 +195,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, B = p.c.B;
-  const int U = p.c.Hkv * p.nblk;  // units of a sequence
+  const int group = cta / p.lanes, ulane = cta - group * p.lanes, groups = gridDim.x / p.lanes;
+  const int U = p.c.Hkv * p.nblk / p.lanes;  // units of a sequence in a lane: ulane + lanes * (0 .. U - 1)
 
-  // ---- this CTA's share [s0, s1) of the list, in which a unit counts its tiles and c0
+  // ---- this group's share [s0, s1) of the list, in which a unit counts its tiles and c0
   long long* red = reinterpret_cast<long long*>(smem);
   auto tiles_of = [&](int b) { return b < B ? paged_tiles<TK>(p, cache_length(p.c, b)) : 0; };
   auto packed = [](int nt) { return (static_cast<long long>(nt) << 32) + (nt != 0); };  // tiles, sequences with keys
@@ -203,12 +209,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   if (lane == 0) red[warp] = sum;
   __syncthreads();
   sum = red[0] + red[1] + red[2] + red[3];
-  const int c0 = (sum >> 32) * U >= 2LL * gridDim.x ? 1 : 0;  // few tiles: one for each CTA
+  const int c0 = (sum >> 32) * U >= 2LL * groups ? 1 : 0;  // few tiles: one for each CTA
   auto cost = [&](long long x) { return ((x >> 32) + (x & 0xffffffffLL) * c0) * U; };
   const long long W = cost(sum);
-  // CTAs with a share: c0 + 1 or more, so that each holds a tile
-  const long long G = min(static_cast<long long>(gridDim.x), W / (c0 + 1));
-  const long long s0 = cta < G ? cta * W / G : 0, s1 = cta < G ? (cta + 1) * W / G : 0;
+  // groups with a share: c0 + 1 or more, so that each holds a tile
+  const long long G = min(static_cast<long long>(groups), W / (c0 + 1));
+  const long long s0 = group < G ? group * W / G : 0, s1 = group < G ? (group + 1) * W / G : 0;
 
   // rows of sequences without keys
   for (int b = cta; b < B; b += gridDim.x) {
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       p.lse[static_cast<long long>(b) * p.H * p.Nq + r] = -INFINITY;
     }
   }
-  if (cta >= G) {
+  if (group >= G) {
     if (tid == 0) p.split[cta] = make_int4(0, 0, 0, 0);
     return;
   }
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     Tile t = {-1, 0, 0, 0, 0, 0, 0};
     if (n >= cnt) return t;
     t.b = fb;
-    t.u = fu;
+    t.u = fu * p.lanes + ulane;
     t.L = fL;
     t.key0 = paged_first_key(p, fL) + ft * TK;
     t.flags = (ft == 0 ? kFlagUnitStart : 0) | (ft == fnt - 1 ? kFlagUnitEnd | kFlagSegEnd : 0) |
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     if (n == cnt - 1 && tid == 0) {
       int4 s = make_int4(0, 0, 0, 0);
       if (seg_starts_unit && !(flags & kFlagUnitEnd)) {  // goes on in the next CTAs
-        s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - cta + 1, 0);
+        s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - group + 1, 0);
       }
       p.split[cta] = s;
     }
@@ -812,7 +818,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 
 // Joins the partials of the units that several CTAs share: block (c, y) the
 // unit that starts in CTA c, 8 rows of it, a warp each.  Partial 0 is CTA c's
-// second slot, the others are the following CTAs' first.
+// second slot, the others are the lane's following CTAs' first.
 template <int D, bool kQuant>
 __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(const PagedParams p, int rows_unit) {
   constexpr int E = D / 32;
@@ -825,7 +831,7 @@ __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(c
   const int kh = s.y / p.nblk, r = (s.y % p.nblk) * rows_unit + rloc;
   if (rloc >= rows_unit || r >= p.R) return;
   auto at = [&](int i) {
-    return (static_cast<long long>(2) * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.prow + rloc;
+    return (static_cast<long long>(2) * (blockIdx.x + i * p.lanes) + (i == 0 ? 1 : 0)) * p.prow + rloc;
   };
   float m = -INFINITY, l = 0.f, u = 0x1p-126f, acc[E];  // u: the accumulators' unit, the largest so far
 #pragma unroll
