@@ -28,6 +28,8 @@
 // with the batch -- for paged_combine_kernel.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_sm100.cuh"
 
 namespace fa {
@@ -107,12 +109,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 template <bool kHalf>
 __device__ __forceinline__ void mma16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t* b) {
   if (kHalf)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
@@ -135,17 +137,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t* lo, uint32_t
       : "=r"(*lo), "=r"(*hi)
       : "r"(x));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-
 // Byte of the 16-byte unit `chunk` of key row `key` in a staged tile.  K: eight
 // lanes read keys (2m, 2m + 1) x 4 consecutive units.  V: bf16, eight keys x
 // one unit (ldmatrix); e4m3, keys (0, 2, 4, 6) + const x units (2c, 2c + 1).
@@ -475,11 +466,16 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       free_hi = L < p.Nq ? 0 : (p.causal ? L - p.Nq + 1 : (p.window < 0 ? L : min(L, L - p.Nq + p.window + 1)));
     }
 
-    const uint32_t sK = smem0 + (n % ST) * C::kStageBytes, sV = sK + C::kTileBytes;
-    const float* scl = reinterpret_cast<const float*>(smem + (n % ST) * C::kStageBytes + 2 * C::kTileBytes);
-    bool edge = key0 < free_lo || key0 + TK > free_hi;
+    const uint8_t* pK = smem + (n % ST) * C::kStageBytes;
+    const uint8_t* pV = pK + C::kTileBytes;
+    const uint32_t sV = paged_smem(pV);
+    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes);
+    bool some = key0 < free_lo || key0 + TK > free_hi;
 #pragma unroll
-    for (int i = 0; i < TK / 32; ++i) edge |= t.valid[i] != 0xffffffffu;
+    for (int i = 0; i < TK / 32; ++i) some |= t.valid[i] != 0xffffffffu;
+    // the steps of a tile; kEdge: some row may not see some key of it
+    auto steps = [&](auto edge_tile) {
+      constexpr bool edge = decltype(edge_tile)::value;
 #pragma unroll 1
     for (int s = 0; s < TK / KW / (16 * KS); ++s) {
       const int kb = (kw * (TK / KW / (16 * KS)) + s) * 16 * KS;
@@ -498,8 +494,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       for (int i = 0; i < (kQuant ? D / 64 : D / 32); ++i)
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const uint4 a = lds128(sK + k_at<RB>(kb + 16 * k + rq, qd + 4 * i)),
-                      b = lds128(sK + k_at<RB>(kb + 16 * k + rq + 8, qd + 4 * i));
+          const uint4 a = *reinterpret_cast<const uint4*>(pK + k_at<RB>(kb + 16 * k + rq, qd + 4 * i)),
+                      b = *reinterpret_cast<const uint4*>(pK + k_at<RB>(kb + 16 * k + rq + 8, qd + 4 * i));
           const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
           if (kQuant) {
 #pragma unroll
@@ -549,7 +545,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
                 sc[k][nb][e] = -INFINITY;
             }
       }
-      auto on = [&](int k, int nb, int e) { return ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
+      auto on = [&](int k, int nb, int e) { return !edge || ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
       // ---- running maximum: moved only when it grows by more than 8 (weights
       // stay below 2^8).  Quantised: weights reach the second product as f16
       // multiples of the largest value scale so far (vref, a power of two above
@@ -643,13 +639,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           for (int y = 0; y < 4; ++y) {
             const int key = kk + 2 * qd + (y & 1) + 8 * (y >> 1);
             if (D == 128) {
-              const uint4 v = lds128(sV + v_at<RB, kQuant>(key, rq));
+              const uint4 v = *reinterpret_cast<const uint4*>(pV + v_at<RB, kQuant>(key, rq));
               w[y][0] = v.x;
               w[y][1] = v.y;
               w[y][2 % (D / 32)] = v.z;
               w[y][3 % (D / 32)] = v.w;
             } else {
-              const uint2 v = lds64(sV + v_at<RB, kQuant>(key, rq >> 1) + (rq & 1) * 8);
+              const uint2 v = *reinterpret_cast<const uint2*>(pV + v_at<RB, kQuant>(key, rq >> 1) + (rq & 1) * 8);
               w[y][0] = v.x;
               w[y][1] = v.y;
             }
@@ -686,11 +682,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           }
           if (!edge || !__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-            for (int x = 0; x < DT; ++x) {
-              uint32_t a[4];
-              ldmatrix_x4_trans(a, at ^ (x << 5));
+            for (int x0 = 0; x0 < DT; x0 += 4) {
+              uint32_t a[4][4];
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x], a[0], a[1], a[2], a[3], pb[k][nb]);
+              for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], at ^ ((x0 + x) << 5));
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x0 + x], a[x][0], a[x][1], a[x][2], a[x][3], pb[k][nb]);
             }
             continue;
           }
@@ -727,6 +726,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           }
       }
     }
+
+    };
+    if (some)
+      steps(std::true_type{});
+    else
+      steps(std::false_type{});
 
     if (!(flags & kFlagSegEnd)) continue;
     // ---- the segment's end: the KW warps of a row group join their states in tile n's stage
