@@ -15,6 +15,12 @@
 #include "fwd_sm100.cuh"
 #include "simt_f32.cuh"
 
+namespace fa {  // paged_api.cu: the same for its kernels
+cudaError_t paged_take_status(unsigned int* v);
+cudaError_t paged_set_wait_limit(unsigned long long ns);
+cudaError_t paged_set_stall(int on);
+}  // namespace fa
+
 namespace {
 
 constexpr int kAbiVersion = 101;
@@ -1036,19 +1042,26 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
 
 fa_status fa_debug_set_wait_limit(unsigned long long ns) {
   const unsigned long long v = ns ? ns : fa::kWaitLimitNs;
-  return cudaMemcpyToSymbol(fa::g_wait_limit_ns, &v, sizeof(v)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaMemcpyToSymbol(fa::g_wait_limit_ns, &v, sizeof(v)) == cudaSuccess &&
+                 fa::paged_set_wait_limit(v) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 fa_status fa_debug_set_stall(int on) {
   const int v = on ? 1 : 0;
-  return cudaMemcpyToSymbol(fa::g_debug_stall, &v, sizeof(v)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaMemcpyToSymbol(fa::g_debug_stall, &v, sizeof(v)) == cudaSuccess && fa::paged_set_stall(v) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 fa_status fa_last_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
-  unsigned int v = 0, zero = 0;
+  unsigned int v = 0, paged = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, fa::g_status, sizeof(v)) != cudaSuccess) return FA_ERR_CUDA;
+  if (fa::paged_take_status(&paged) != cudaSuccess) return FA_ERR_CUDA;
   if (v != 0 && cudaMemcpyToSymbol(fa::g_status, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
+  v |= paged;
   if (v & fa::kStatusTimeout) return FA_ERR_TIMEOUT;
   return v ? FA_ERR_CUDA : FA_OK;
 }

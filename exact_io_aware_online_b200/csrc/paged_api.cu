@@ -3,6 +3,7 @@
 // that the dense kernels' sources (which their captured profiles are keyed by)
 // do not depend on it.  Like there, every entry point validates on the host
 // first and enqueues nothing when an argument is bad.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -79,6 +80,12 @@ fa_status check_strides(const fa_strides& in, long long n0, long long n1, long l
   return FA_OK;
 }
 
+void magic(int divisor, uint32_t* mul, int* shift) {  // see page_of()
+  *shift = 0;
+  while ((1LL << *shift) < divisor) ++*shift;
+  *mul = static_cast<uint32_t>(((1ULL << (31 + *shift)) + divisor - 1) / divisor);
+}
+
 // `written`: the pages are an output.
 fa_status check_cache(const fa_paged_cache* c, fa_dtype dtype, bool written, fa::CacheParams* p) {
   if (!c || !c->k_pages || !c->v_pages || !c->page_table || !c->seqlens) return FA_ERR_INVALID_ARG;
@@ -114,9 +121,7 @@ fa_status check_cache(const fa_paged_cache* c, fa_dtype dtype, bool written, fa:
   p->num_pages = c->num_pages;
   p->page_size = c->page_size;
   p->max_pages = c->max_pages;
-  p->page_shift = 0;
-  while ((1LL << p->page_shift) < c->page_size) ++p->page_shift;
-  p->page_mul = static_cast<uint32_t>(((1ULL << (31 + p->page_shift)) + c->page_size - 1) / c->page_size);
+  magic(c->page_size, &p->page_mul, &p->page_shift);
   return FA_OK;
 }
 
@@ -158,6 +163,42 @@ fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_st
                : launch(fa::cache_move_kernel<128, false, kWrite>, grid, block, 0, st, false, p);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(f)
+               : nullptr;
+  }();
+  return fn;
+}
+
+// Pages [num_pages, Hkv, page_size, d] in boxes of `box` tokens of one page and
+// head: rows of 128 bytes (64 where a row has no more) with the swizzle of that
+// width.  Tokens behind the page's end and a page number of num_pages read as zero.
+bool page_map(CUtensorMap* m, const void* base, const fa::CacheParams& c, int d, bool quant, int box) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const int es = quant ? 1 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.pages.n) * es, static_cast<cuuint64_t>(c.pages.h) * es,
+                                 static_cast<cuuint64_t>(c.pages.b) * es};
+  const int inner = std::min(d * es, 128);
+  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(inner / es), static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return enc(m, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+             dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The workspace: split[CTAs] (int4), part_m[2 * CTAs][rows] (float4), part_o[2 * CTAs][rows][d] (float)
 struct PagedOffsets {
   size_t part_m, part_o, bytes;
@@ -173,7 +214,7 @@ PagedOffsets paged_offsets(int rows, int d) {
 int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // rows of a unit
 
 template <int D, bool kQuant, int NB, int RG>
-fa_status launch_paged(fa::PagedParams p, double tiles, cudaStream_t st) {
+fa_status launch_paged(fa::PagedParams p, const CUtensorMap* maps, double tiles, cudaStream_t st) {
   using C = fa::PagedCfg<D, kQuant, NB, RG>;
   const auto kernel = fa::paged_kernel<D, kQuant, NB, RG>;
   int dev = 0;
@@ -191,19 +232,19 @@ fa_status launch_paged(fa::PagedParams p, double tiles, cudaStream_t st) {
   while (units % p.lanes != 0 || most % p.lanes > most / 16) --p.lanes;
   // no more groups than the lengths could give tiles
   const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles));
-  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, p);
+  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, maps[0], maps[1], p);
   if (s != FA_OK) return s;
   const dim3 grid(ctas, (p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
   return launch(fa::paged_combine_kernel<D, kQuant>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, C::kRows);
 }
 
 template <int D, bool kQuant>
-fa_status launch_paged_rows(const fa::PagedParams& p, double tiles, cudaStream_t st) {
+fa_status launch_paged_rows(const fa::PagedParams& p, const CUtensorMap* maps, double tiles, cudaStream_t st) {
   switch (paged_rows(p.R)) {
-    case 8: return launch_paged<D, kQuant, 1, 1>(p, tiles, st);
-    case 16: return launch_paged<D, kQuant, 2, 1>(p, tiles, st);
-    case 32: return launch_paged<D, kQuant, 2, 2>(p, tiles, st);
-    default: return launch_paged<D, kQuant, 2, 4>(p, tiles, st);
+    case 8: return launch_paged<D, kQuant, 1, 1>(p, maps, tiles, st);
+    case 16: return launch_paged<D, kQuant, 2, 1>(p, maps, tiles, st);
+    case 32: return launch_paged<D, kQuant, 2, 2>(p, maps, tiles, st);
+    default: return launch_paged<D, kQuant, 2, 4>(p, maps, tiles, st);
   }
 }
 
@@ -213,6 +254,20 @@ bool paged_sizes_ok(int B, int H, int Hkv, int Nq) {
 }
 
 }  // namespace
+
+// This translation unit's copies of the device status word and the debugging
+// switches, for the entry points that report and set them (fa_api.cu).
+namespace fa {
+
+cudaError_t paged_take_status(unsigned int* v) {
+  const unsigned int zero = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(v, g_status, sizeof(*v));
+  return e != cudaSuccess || *v == 0 ? e : cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+}
+cudaError_t paged_set_wait_limit(unsigned long long ns) { return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns)); }
+cudaError_t paged_set_stall(int on) { return cudaMemcpyToSymbol(g_debug_stall, &on, sizeof(on)); }
+
+}  // namespace fa
 
 extern "C" {
 
@@ -269,12 +324,21 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.split = reinterpret_cast<int4*>(ws);
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
-  const long long cap = static_cast<long long>(cache->max_pages) * cache->page_size;
+  p.pad_page = (cache->page_size + 7) & ~7;
+  p.box_log = p.pad_page % 32 == 0 ? 5 : p.pad_page % 16 == 0 ? 4 : 3;
+  magic(p.pad_page, &p.pad_mul, &p.pad_shift);
+  const long long cap = static_cast<long long>(cache->max_pages) * p.pad_page;
+  if (cap > (1LL << 30)) return FA_ERR_UNSUPPORTED;  // padded positions are 32-bit too
   const double tiles = static_cast<double>((cap + 63) / 64) * B * Hkv * p.nblk;  // at most
-  if (tiles / 148 > 1e9) return FA_ERR_UNSUPPORTED;  // a CTA counts its tiles in 32 bits
+  // tiles are counted in 32 bits: a CTA's, and all sequences' of one head
+  if (tiles / 148 > 1e9 || static_cast<double>((cap + 63) / 64) * B > 2e9) return FA_ERR_UNSUPPORTED;
   const bool quant = cache->dtype == FA_CACHE_E4M3;
-  if (d == 64) return quant ? launch_paged_rows<64, true>(p, tiles, st) : launch_paged_rows<64, false>(p, tiles, st);
-  return quant ? launch_paged_rows<128, true>(p, tiles, st) : launch_paged_rows<128, false>(p, tiles, st);
+  CUtensorMap maps[2];
+  if (!page_map(&maps[0], cache->k_pages, p.c, d, quant, 1 << p.box_log) ||
+      !page_map(&maps[1], cache->v_pages, p.c, d, quant, 1 << p.box_log))
+    return FA_ERR_CUDA;
+  if (d == 64) return quant ? launch_paged_rows<64, true>(p, maps, tiles, st) : launch_paged_rows<64, false>(p, maps, tiles, st);
+  return quant ? launch_paged_rows<128, true>(p, maps, tiles, st) : launch_paged_rows<128, false>(p, maps, tiles, st);
 }
 
 }  // extern "C"

@@ -21,24 +21,29 @@
 // rows, the 32-byte sectors of the scales are read from DRAM once, and blocks
 // of rows share their keys in L2.  The tiles of all sequences form one list, and
 // group c of G takes its c-th even share, whatever the lengths (beginning a
-// unit counts as much as a tile): each CTA walks its tiles through a cp.async
-// ring that runs on from one unit into the next.  A unit that lies in one share
-// is finished by its CTA; one that several share leaves a partial (m, l,
+// unit counts as much as a tile).  In each CTA one warp walks the share, looks
+// pages up and keeps a ring of tiles loading (TMA boxes of 8 to 32 tokens, each
+// inside a page; scales by cp.async), on from one unit into the next; four
+// warps compute.  A unit that lies in one share is finished by its CTA; one that several share leaves a partial (m, l,
 // accumulator) per CTA -- at most two per CTA, so the workspace does not grow
 // with the batch -- for paged_combine_kernel.
+//
+// Positions inside the kernel are padded: a page counts as page_size rounded up
+// to 8 tokens, so that a box never spans two pages; the slots that do not exist
+// are zero-filled by the TMA and masked.
 #pragma once
 
 #include <type_traits>
 
 #include "cache_sm100.cuh"
+#include "sm100_ptx.cuh"
 
 namespace fa {
 
-constexpr int kPagedThreads = 128;  // 4 warps
+constexpr int kPagedWarps = 4;      // that compute; one more loads
+constexpr int kPagedThreads = 32 * (kPagedWarps + 1);
 constexpr int kPagedMaxCtas = 444;  // three on each of 148 SMs
 constexpr int kPagedCombineRows = 8;
-constexpr int kPagedRing = 8;       // descriptions of tiles: those staged, the one computed and the next one
-constexpr int kPagedOffs = 4;       // tiles' row offsets, from store() to issue()
 
 struct PagedParams {
   CacheParams c;
@@ -51,6 +56,10 @@ struct PagedParams {
   int causal, window;
   int R, nblk;     // rows of a kv head (g * Nq), units they make
   int lanes;       // CTAs of a group: a divisor of Hkv * nblk
+  int pad_page;    // page_size rounded up to a multiple of 8
+  uint32_t pad_mul;  // pos / pad_page, as CacheParams::page_mul
+  int pad_shift;
+  int box_log;     // log2 of the tokens of a TMA box: 3 to 5
   int prow;        // rows of a partial: min(R, rows of a unit)
   float* part_o;   // [2 * G][prow][D]
   float4* part_m;  // [2 * G][prow]: m, l, unit of the accumulator
@@ -58,40 +67,33 @@ struct PagedParams {
 };
 
 // A warp holds NB blocks of 8 rows; RG groups of warps hold different rows, the
-// 4 / RG warps of a group share each tile's keys.
+// kPagedWarps / RG warps of a group share each tile's keys.
 template <int D, bool kQuant, int NB, int RG>
 struct PagedCfg {
   static constexpr int kRows = 8 * NB * RG;  // rows of a unit
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
   static constexpr int kTile = kRowBytes == 256 ? 64 : 128;  // keys
+  static constexpr int kPart = kRowBytes == 256 ? 128 : kRowBytes;  // bytes of a row in a TMA box (its swizzle's width)
   static constexpr int kTileBytes = kTile * kRowBytes;
-  static constexpr int kScaleBytes = kQuant ? kTile * 4 : 0;
-  static constexpr int kStageBytes = 2 * kTileBytes + 2 * kScaleBytes;
-  static constexpr int kCtas = kStageBytes >= 32768 || (D == 128 && NB == 2) ? 2 : 3;  // of an SM
-  static constexpr int kStages = 3;
+  static constexpr int kStageBytes = 2 * kTileBytes + (kQuant ? 1024 : 0);  // K, V, scales of K and of V
+  static constexpr int kCtas = D == 128 && NB == 2 ? 2 : 3;  // of an SM
+  static constexpr int kStages = (226 * 1024 / kCtas - 2048) / kStageBytes < 4 ? (226 * 1024 / kCtas - 2048) / kStageBytes : 4;
   static constexpr int kMergeStride = D + 4;  // floats; 2 * stride = 8 mod 32: a warp's stores meet every bank once
-  static constexpr int kStatBytes = 4 * 8 * NB * 16;
-  static constexpr int kOffsBytes = kPagedOffs * kTile * 8;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kStatBytes + (kQuant ? 2 : 1) * kOffsBytes + kPagedRing * 48;
-  static_assert(kStages + 2 <= kPagedRing && kStages <= kPagedOffs, "a tile's description outlives its copies");
-  static_assert(4 * 8 * kMergeStride * 4 <= kStageBytes, "the warps' accumulators are joined in a stage");
+  static constexpr int kStatBytes = kPagedWarps * 8 * NB * 16;
+  static constexpr int kSmemBytes = kStages * (kStageBytes + 16 + 48) + kStatBytes + 16 + 128;
+  static_assert(kStages >= 2, "a tile loads while another is computed");
+  static_assert(kPagedWarps * 8 * kMergeStride * 4 <= 2 * kTileBytes, "the warps' accumulators are joined in a stage");
 };
 
-__device__ __forceinline__ uint32_t paged_smem(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 (or 4) bytes to shared memory, zeros when !on.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
+// 4 bytes to shared memory, zero when !on.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The barrier counts an arrival once this thread's cp.async copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -125,6 +127,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+__device__ __forceinline__ void ldmatrix_x4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -137,60 +145,71 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t* lo, uint32_t
       : "=r"(*lo), "=r"(*hi)
       : "r"(x));
 }
-// Byte of the 16-byte unit `chunk` of key row `key` in a staged tile.  K: eight
-// lanes read keys (2m, 2m + 1) x 4 consecutive units.  V: bf16, eight keys x
-// one unit (ldmatrix); e4m3, keys (0, 2, 4, 6) + const x units (2c, 2c + 1).
-// The exclusive-or puts each such set into different banks (but for V rows of
-// 64 bytes, which are read in pairs).
-template <int kRowBytes>
-__device__ __forceinline__ uint32_t k_at(int key, int chunk) {
-  return key * kRowBytes + (kRowBytes == 64 ? chunk << 4 : (chunk ^ ((key & 1) << 2)) << 4);
+// Padded positions: pos + (pad_page - page_size) for every page before it.
+__device__ __forceinline__ int paged_pad(const PagedParams& p, int pos) {
+  return p.pad_page == p.c.page_size ? pos : pos + page_of(p.c, pos) * (p.pad_page - p.c.page_size);
 }
-template <int kRowBytes, bool kQuant>
-__device__ __forceinline__ uint32_t v_at(int key, int chunk) {
-  const int x = !kQuant ? key & 7 : kRowBytes == 128 ? key & 6 : key & 2;
-  return key * kRowBytes + ((chunk ^ x) << 4);
-}
-
-// First key that some row of a sequence of length L may see, and its tiles.
-__device__ __forceinline__ int paged_first_key(const PagedParams& p, int L) {
-  return p.window < 0 ? 0 : max(0, max(L - p.Nq, 0) - p.window);
+// The padded positions [x, y) of a sequence of length L that some row may see;
+// x is the beginning of a box.
+__device__ __forceinline__ int2 paged_span(const PagedParams& p, int L) {
+  if (L == 0) return make_int2(0, 0);
+  const int first = p.window < 0 ? 0 : max(0, max(L - p.Nq, 0) - p.window);
+  return make_int2(paged_pad(p, first) >> p.box_log << p.box_log, paged_pad(p, L - 1) + 1);
 }
 template <int kTile>
 __device__ __forceinline__ int paged_tiles(const PagedParams& p, int L) {
-  return (L - paged_first_key(p, L) + kTile - 1) / kTile;
+  const int2 s = paged_span(p, L);
+  return (s.y - s.x + kTile - 1) / kTile;
 }
 
-struct PagedDesc {  // a tile, as the front of the pipeline describes it to the rest
-  int b, unit, key0, flags, L;
-  uint32_t valid[4];  // keys that exist: in range and on a page
+__device__ __forceinline__ int paged_slot(const PagedParams& p, int padded) {  // the token inside its page
+  return padded - static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(padded)) * p.pad_mul) >>
+                                   (31 + p.pad_shift)) * p.pad_page;
+}
+
+struct PagedDesc {  // a tile, as the loading warp describes it to the others
+  int b, unit, key0, end, flags, L;
+  uint32_t boxes;         // those that are on a page
+  int next_b, next_unit;  // of the tile after it
   int pad[3];
 };
 constexpr int kFlagUnitStart = 1, kFlagUnitEnd = 2, kFlagSegEnd = 4;
 
 template <int D, bool kQuant, int NB, int RG>
 __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kCtas)
-    paged_kernel(const PagedParams p) {
+    paged_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ PagedParams p) {
   using C = PagedCfg<D, kQuant, NB, RG>;
-  constexpr int KW = 4 / RG;                  // warps that share a tile's keys
+  constexpr int KW = kPagedWarps / RG;        // warps that share a tile's keys
   constexpr int DT = D / 16;                  // row tiles of O^T = V^T P^T
   constexpr int QS = D / 16;                  // k-steps of S^T = K Q^T
-  constexpr int ST = C::kStages, RB = C::kRowBytes, TK = C::kTile;
+  constexpr int ST = C::kStages, RB = C::kRowBytes, PB = C::kPart, TK = C::kTile;
   constexpr int KS = TK / KW >= 32 ? 2 : 1;   // groups of 16 keys that a warp takes together
   constexpr int ES = kQuant ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem[];
-  float4* stat = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);  // [4 warps][8 * NB rows]: m, l, unit
-  long long* offs = reinterpret_cast<long long*>(stat + 4 * 8 * NB);     // [kPagedOffs][TK] byte offset of a row, -1: none
-  long long* soffs = offs + kPagedOffs * TK;                         // [kPagedOffs][TK] element offset of its scale
-  PagedDesc* desc = reinterpret_cast<PagedDesc*>(kQuant ? soffs + kPagedOffs * TK : soffs);  // [ring]
+  float4* stat = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);     // [warps][8 * NB rows]: m, l, unit
+  PagedDesc* desc = reinterpret_cast<PagedDesc*>(stat + kPagedWarps * 8 * NB);  // [ST]
+  uint64_t* full = reinterpret_cast<uint64_t*>(desc + ST);                  // [ST]
+  uint64_t* empty = full + ST;                                              // [ST]
+  uint64_t* joined = empty + ST;
+  volatile int* abort = reinterpret_cast<int*>(joined + 1);
+  long long* red = reinterpret_cast<long long*>(joined + 2);                // [16]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, B = p.c.B;
   const int group = cta / p.lanes, ulane = cta - group * p.lanes, groups = gridDim.x / p.lanes;
   const int U = p.c.Hkv * p.nblk / p.lanes;  // units of a sequence in a lane: ulane + lanes * (0 .. U - 1)
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(full + i, kQuant ? 33 : 1);
+      mbar_init(empty + i, kPagedWarps);
+    }
+    mbar_init(joined, kPagedWarps);
+    *abort = 0;
+    fence_mbar_init();
+  }
 
   // ---- this group's share [s0, s1) of the list, in which a unit counts its tiles and c0
-  long long* red = reinterpret_cast<long long*>(smem);
   auto tiles_of = [&](int b) { return b < B ? paged_tiles<TK>(p, cache_length(p.c, b)) : 0; };
   auto packed = [](int nt) { return (static_cast<long long>(nt) << 32) + (nt != 0); };  // tiles, sequences with keys
   long long sum = 0;
@@ -199,7 +218,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) red[warp] = sum;
   __syncthreads();
-  sum = red[0] + red[1] + red[2] + red[3];
+  sum = 0;
+  for (int w = 0; w < kPagedThreads / 32; ++w) sum += red[w];
   const int c0 = (sum >> 32) * U >= 2LL * groups ? 1 : 0;  // few tiles: one for each CTA
   auto cost = [&](long long x) { return ((x >> 32) + (x & 0xffffffffLL) * c0) * U; };
   const long long W = cost(sum);
@@ -224,12 +244,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   }
 
   // ---- the front cursor: sequence, unit and tile of s0; the tiles up to s1
-  int fb, fu, ft, fL, fnt, fLnext, cnt;
+  int fb, fu, ft, cnt;
   long long last_end;  // where the unit that s1 lies in ends
   {
     long long base = 0;
     __syncthreads();
-    if (tid == 0) red[8] = (sum >> 32) * U, red[9] = W;  // s1 at the very end
+    if (tid == 0) red[12] = (sum >> 32) * U, red[13] = W;  // s1 at the very end
     for (int at = 0;; at += kPagedThreads) {
       const int b = at + tid, nt = tiles_of(b);
       long long incl = packed(nt);
@@ -253,169 +273,197 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           const int t = max(0, off - c0);
           const long long done = (first >> 32) * U + static_cast<long long>(u) * nt + t;  // tiles before it
           if (e) {
-            red[8] = done;
-            red[9] = at_s - off + nt + c0;
+            red[12] = done;
+            red[13] = at_s - off + nt + c0;
           } else {
-            red[4] = b;
-            red[5] = u;
-            red[6] = t;
-            red[7] = done;
+            red[8] = b;
+            red[9] = u;
+            red[10] = t;
+            red[11] = done;
           }
         }
       }
-      base += red[0] + red[1] + red[2] + red[3];
+      for (int w = 0; w < kPagedThreads / 32; ++w) base += red[w];
       if (s1 < cost(base) || at + kPagedThreads >= B) break;  // found (uniform)
     }
     __syncthreads();
-    fb = static_cast<int>(red[4]);
-    fu = static_cast<int>(red[5]);
-    ft = static_cast<int>(red[6]);
-    cnt = static_cast<int>(red[8] - red[7]);
-    last_end = red[9];
-    __syncthreads();
-    fL = cache_length(p.c, fb);
-    fnt = paged_tiles<TK>(p, fL);
-    fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
+    fb = static_cast<int>(red[8]);
+    fu = static_cast<int>(red[9]);
+    ft = static_cast<int>(red[10]);
+    cnt = static_cast<int>(red[12] - red[11]);
+    last_end = red[13];
   }
-  const int frow = tid & (TK - 1);
-  struct Tile {  // a tile as fetch() leaves it for store(): this thread's row
-    int page, slot, b, u, key0, flags, L;
-  };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // fetch(n): loads the page of this thread's row of tile n and advances the cursor
-  auto fetch = [&](int n) {
-    Tile t = {-1, 0, 0, 0, 0, 0, 0};
-    if (n >= cnt) return t;
-    t.b = fb;
-    t.u = fu * p.lanes + ulane;
-    t.L = fL;
-    t.key0 = paged_first_key(p, fL) + ft * TK;
-    t.flags = (ft == 0 ? kFlagUnitStart : 0) | (ft == fnt - 1 ? kFlagUnitEnd | kFlagSegEnd : 0) |
-              (n == cnt - 1 ? kFlagSegEnd : 0);
-    const int pos = t.key0 + frow;
-    if (tid < TK && pos < fL) {
-      const int i = page_of(p.c, pos);
-      t.slot = pos - i * p.c.page_size;
-      t.page = p.c.table[fb * p.c.table_stride + i];
-    }
-    if (++ft == fnt) {
-      ft = 0;
-      if (++fu == U) {
-        fu = 0;
-        if (n + 1 < cnt) {  // the next sequence with keys (there is one: tiles are left)
-          do {
-            ++fb;
-            fL = fLnext;
-            fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
-            fnt = paged_tiles<TK>(p, fL);
-          } while (fnt == 0 && fb < B - 1);
+  if (warp == kPagedWarps) {
+    // ---- the loading warp
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+    if (*static_cast<volatile int*>(&g_debug_stall)) return;
+    const int box = 1 << p.box_log;
+    int fL = cache_length(p.c, fb), fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
+    int2 span = paged_span(p, fL);
+    int fnt = paged_tiles<TK>(p, fL);
+    struct Tile {
+      int b, u, key0, end, flags, L;
+      int page, slot;  // of box `lane`
+    };
+    // the n-th tile; moves the cursor on
+    auto fetch = [&](int n) {
+      Tile t = {0, 0, 0, 0, 0, 0, -1, 0};
+      if (n >= cnt) return t;
+      t.b = fb;
+      t.u = fu * p.lanes + ulane;
+      t.L = fL;
+      t.key0 = span.x + ft * TK;
+      t.end = span.y;
+      t.flags = (ft == 0 ? kFlagUnitStart : 0) | (ft == fnt - 1 ? kFlagUnitEnd | kFlagSegEnd : 0) |
+                (n == cnt - 1 ? kFlagSegEnd : 0);
+      const int pos = t.key0 + (lane << p.box_log);
+      if (lane < TK >> p.box_log && pos < t.end) {
+        const int i = static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(pos)) * p.pad_mul) >>
+                                       (31 + p.pad_shift));
+        t.slot = pos - i * p.pad_page;
+        t.page = p.c.table[fb * p.c.table_stride + i];
+      }
+      if (++ft == fnt) {
+        ft = 0;
+        if (++fu == U) {
+          fu = 0;
+          if (n + 1 < cnt) {  // the next sequence with keys (there is one: tiles are left)
+            do {
+              ++fb;
+              fL = fLnext;
+              fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
+              fnt = paged_tiles<TK>(p, fL);
+            } while (fnt == 0 && fb < B - 1);
+            span = paged_span(p, fL);
+          }
         }
       }
-    }
-    return t;
-  };
-  // store(n): the row's offsets and the tile's description, for issue() and compute()
-  auto store = [&](int n, const Tile& f) {
-    if (n >= cnt) return;
-    const bool on = f.page >= 0 && f.page < p.c.num_pages;
-    const int kh = p.nblk == 1 ? f.u : f.u / p.nblk;
-    if (tid < TK) {
-      offs[(n % kPagedOffs) * TK + tid] = on ? p.c.pages.row(f.page, kh, f.slot) * ES : -1;
-      if (kQuant) soffs[(n % kPagedOffs) * TK + tid] = on ? p.c.scales.row(f.page, kh, f.slot) : -1;
-      const uint32_t m = __ballot_sync(0xffffffffu, on);
-      PagedDesc& t = desc[n % kPagedRing];
-      if (lane == 0) t.valid[warp] = m;
-      if (tid == 0) {
-        t.b = f.b;
-        t.unit = f.u;
-        t.key0 = f.key0;
-        t.flags = f.flags;
-        t.L = f.L;
+      return t;
+    };
+    Tile cur = fetch(0);
+    int st = 0, ph = 1;
+    int n = 0;
+    for (; n < cnt; ++n) {
+      const Tile next = fetch(n + 1);
+      if (!__all_sync(0xffffffffu, n < ST || mbar_wait(empty + st, ph, abort))) break;
+      const bool on = cur.page >= 0 && cur.page < p.c.num_pages;
+      const uint32_t boxes = __ballot_sync(0xffffffffu, on);
+      // boxes up to the end of the last group of 32 keys; those on no page are filled with zeros
+      const int live = min(TK, (cur.end - cur.key0 + 31) & ~31) >> p.box_log;
+      const int kh = p.nblk == 1 ? cur.u : cur.u / p.nblk;
+      uint8_t* dst = smem + st * C::kStageBytes;
+      if (lane == 0) {
+        PagedDesc& t = desc[st];
+        t.b = cur.b;
+        t.unit = cur.u;
+        t.key0 = cur.key0;
+        t.end = cur.end;
+        t.flags = cur.flags;
+        t.L = cur.L;
+        t.boxes = boxes;
+        t.next_b = next.b;
+        t.next_unit = next.u;
+        mbar_arrive_expect_tx(full + st, (live << p.box_log) * 2 * RB);
       }
-    }
-  };
-  const uint32_t smem0 = paged_smem(smem);
-  // issue(n): the copies of tile n into its stage (always one group, empty past the end)
-  constexpr int CPR = RB / 16, RPI = kPagedThreads / CPR;  // 16-byte units of a row, rows of a pass
-  const int chunk = tid % CPR, crow = tid / CPR;
-  auto issue = [&](int n) {
-    if (n < cnt) {
-      const uint32_t dst = smem0 + (n % ST) * C::kStageBytes;
-      const long long* src = offs + (n % kPagedOffs) * TK + crow;
+      const int page = on ? cur.page : p.c.num_pages;
+      for (int i = 0; i < live; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i), slot = __shfl_sync(0xffffffffu, cur.slot, i);
+        if (lane == 0) {
+          uint8_t* to = dst + (i << p.box_log) * PB;
 #pragma unroll
-      for (int i = 0; i < TK / RPI; ++i) {
-        const int row = crow + i * RPI;
-        const long long off = src[i * RPI];
-        const bool on = off >= 0;
-        const long long at = (on ? off : 0) + chunk * 16;
-        cp_async16(dst + k_at<RB>(row, chunk), p.c.k + at, on);
-        cp_async16(dst + C::kTileBytes + v_at<RB, kQuant>(row, chunk), p.c.v + at, on);
+          for (int h = 0; h < RB / PB; ++h) {
+            tma_load_4d(&map_k, full + st, to + h * TK * PB, h * PB / ES, slot, kh, pg);
+            tma_load_4d(&map_v, full + st, to + h * TK * PB + C::kTileBytes, h * PB / ES, slot, kh, pg);
+          }
+        }
       }
       if (kQuant) {
-        const long long off = soffs[(n % kPagedOffs) * TK + tid], at = off >= 0 ? off : 0;
-        cp_async4(dst + 2 * C::kTileBytes + tid * 4, p.c.ks + at, off >= 0);
-        cp_async4(dst + 2 * C::kTileBytes + (TK + tid) * 4, p.c.vs + at, off >= 0);
+        const long long at = on ? p.c.scales.row(cur.page, kh, cur.slot) : -1;
+        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes);
+#pragma unroll
+        for (int r = lane; r < TK; r += 32) {
+          const int src = r >> p.box_log, in = r & (box - 1);
+          long long off = __shfl_sync(0xffffffffu, at, src);
+          const int slot = __shfl_sync(0xffffffffu, cur.slot, src) + in;
+          const bool here = off >= 0 && slot < p.c.page_size;
+          off = here ? off + in * p.c.scales.n : 0;
+          cp_async4(to + r * 4, p.c.ks + off, here);
+          cp_async4(to + 512 + r * 4, p.c.vs + off, here);
+        }
+        cp_async_arrive(full + st);
       }
+      cur = next;
+      if (++st == ST) st = 0, ph ^= 1;
     }
-    cp_async_commit();
-  };
+    if (kQuant) cp_async_wait_all();
+    for (int i = max(0, n - ST); i < n; ++i)  // the copies under way end before the CTA does
+      mbar_wait_drain(full + i % ST, (i / ST) & 1);
+    return;
+  }
 
-  // ---- a warp's rows and its share of a tile's keys
+  // ---- a computing warp's rows and its share of a tile's keys
   const int rg = warp / KW, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
-  uint32_t qb[NB][QS][2];  // Q^T: row rq of each block, the k index in the order in which a key's 16-byte units come
+  uint32_t qb[NB][QS][2];  // Q^T: row rq of each block, the k index in the order of the K fragments
   float acc[NB][DT][4];    // O^T: columns dcol(x, 0), dcol(x, 1) of V for rows 2 qd, 2 qd + 1
   float m[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2];
-  int rlo[NB][2], rhi[NB][2];  // keys that the thread's rows may see
-  int free_lo = 0, free_hi = 0;  // keys that every row of the unit may see
+  int rlo[NB][2], rhi[NB][2];  // padded positions that the thread's rows may see
+  int free_lo = 0, free_hi = 0;  // those that every row of the unit may see
   bool seg_starts_unit = false, fresh = true;  // fresh: the next tile begins a segment
   auto dcol = [&](int x, int e) { return kQuant ? rq * (D / 8) + 2 * x + e : 16 * x + 8 * e + rq; };
-  // the queries of unit t, as they are in memory
-  auto load_q = [&](const PagedDesc& t) {
-    const int kh = p.nblk == 1 ? t.unit : t.unit / p.nblk, row0 = (t.unit - kh * p.nblk) * C::kRows + rg * 8 * NB;
-    constexpr int W2 = kQuant ? 8 : 4;  // words of q that belong to one 16-byte unit of k
+  // the queries of a unit, as they are in memory: words (8 s + qd, + 4) of a row, or its words 8 s + 2 qd, + 1 where
+  // the K fragments are taken from 16 codes at a time
+  auto load_q = [&](int b, int unit) {
+    const int kh = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - kh * p.nblk) * C::kRows + rg * 8 * NB;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = row0 + nb * 8 + rq;
       const int h = p.Nq == 1 ? r : r / p.Nq;
-      const uint8_t* qr = p.q + 2 * (r < p.R ? p.sq.row(t.b, kh * p.g + h, r - h * p.Nq) : 0);
+      const uint32_t* qr = reinterpret_cast<const uint32_t*>(p.q + 2 * (r < p.R ? p.sq.row(b, kh * p.g + h, r - h * p.Nq) : 0));
 #pragma unroll
-      for (int i = 0; i < D / 2 / W2 / 4; ++i)
-#pragma unroll
-        for (int y = 0; y < W2; y += 4) {
-          const uint4 v = r < p.R ? __ldg(reinterpret_cast<const uint4*>(qr + (qd + 4 * i) * W2 * 4 + y * 4))
-                                  : make_uint4(0, 0, 0, 0);
-          const int s = i * (W2 / 2) + y / 2;
-          qb[nb][s][0] = v.x;
-          qb[nb][s][1] = v.y;
-          qb[nb][s + 1][0] = v.z;
-          qb[nb][s + 1][1] = v.w;
-        }
+      for (int s = 0; s < QS; ++s) {
+        uint2 v = make_uint2(0, 0);
+        if (r < p.R)
+          v = kQuant ? __ldg(reinterpret_cast<const uint2*>(qr + 8 * s + 2 * qd))
+                     : make_uint2(__ldg(qr + 8 * s + qd), __ldg(qr + 8 * s + 4 + qd));
+        qb[nb][s][0] = v.x;
+        qb[nb][s][1] = v.y;
+      }
     }
   };
+  int jph = 0;
+  auto join = [&] {  // the computing warps meet; false: given up
+    __syncwarp();
+    if (lane == 0) mbar_arrive(joined);
+    const bool ok = mbar_wait(joined, jph, abort);
+    jph ^= 1;
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  int st = 0, ph = 0;
+  auto release = [&] {  // this warp is done with the stage
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + st);
+    if (++st == ST) st = 0, ph ^= 1;
+  };
+  // a lane's row in a fragment of 16 keys x 32 bytes; parts of a row are kTile * kPart apart, their 16-byte units
+  // swizzled by the TMA: unit ^ (key & 7) (128 bytes), unit ^ (key / 2 & 3) (64 bytes)
+  auto swz = [](int key) { return PB == 128 ? key & 7 : (key >> 1) & 3; };
+  auto part = [](int i) { return i * 32 / PB * TK * PB; };
+  const int kkey = (lane & 7) + ((lane >> 3) & 1) * 8, vkey = (lane & 7) + ((lane >> 4) << 3);
+  const uint32_t kat = kkey * PB + (((lane >> 4) ^ swz(kkey)) << 4);
+  const uint32_t vat = vkey * PB + ((((lane >> 3) & 1) ^ swz(vkey)) << 4);
+  auto v_at = [&](int key, int byte) {  // of a row of V
+    return byte / PB * TK * PB + key * PB + ((((byte % PB) >> 4) ^ swz(key)) << 4) + (byte & 15);
+  };
 
-  {
-    Tile t[ST];
-#pragma unroll
-    for (int n = 0; n < ST; ++n) t[n] = fetch(n);
-#pragma unroll
-    for (int n = 0; n < ST; ++n) store(n, t[n]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < ST - 1; ++n) issue(n);
-  load_q(desc[0]);
-  Tile next = fetch(ST);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+  load_q(fb, fu * p.lanes + ulane);
   for (int n = 0; n < cnt; ++n) {
-    cp_async_wait<ST - 2>();
-    store(n + ST, next);
-    __syncthreads();  // tile n has landed; everyone is done with tile n - 1
-    issue(n + ST - 1);
-    next = fetch(n + ST + 1);
-
-    const PagedDesc& t = desc[n % kPagedRing];
-    const int key0 = t.key0, flags = t.flags;
+    if (!__all_sync(0xffffffffu, mbar_wait(full + st, ph, abort))) return;
+    const PagedDesc& t = desc[st];
+    const int key0 = t.key0, flags = t.flags, left = t.end - t.key0;
+    const uint32_t boxes = t.boxes, all_boxes = 0xffffffffu >> (32 - (TK >> p.box_log));
     if (fresh) {
       fresh = false;
       seg_starts_unit = flags & kFlagUnitStart;
@@ -454,73 +502,64 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           const int i = p.Nq == 1 ? 0 : r % p.Nq, pos = L - p.Nq + i;
           rlo[nb][c] = 0;
           rhi[nb][c] = 0;  // padding rows see nothing
-          if (r < p.R) {
-            rlo[nb][c] = p.window < 0 ? 0 : max(0, pos - p.window);
-            rhi[nb][c] = pos < 0 ? 0 : (p.causal ? pos + 1 : (p.window < 0 ? L : min(L, pos + p.window + 1)));
+          if (r < p.R && pos >= 0) {
+            rlo[nb][c] = p.window < 0 ? 0 : paged_pad(p, max(0, pos - p.window));
+            rhi[nb][c] = paged_pad(p, (p.causal ? pos : (p.window < 0 ? L - 1 : min(L - 1, pos + p.window)))) + 1;
           }
         }
 #pragma unroll
         for (int x = 0; x < DT; ++x) acc[nb][x][0] = acc[nb][x][1] = acc[nb][x][2] = acc[nb][x][3] = 0.f;
       }
-      free_lo = p.window < 0 ? 0 : max(0, L - 1 - p.window);
-      free_hi = L < p.Nq ? 0 : (p.causal ? L - p.Nq + 1 : (p.window < 0 ? L : min(L, L - p.Nq + p.window + 1)));
+      free_lo = p.window < 0 ? 0 : paged_pad(p, max(0, L - 1 - p.window));
+      free_hi = 0;
+      if (L >= p.Nq)
+        free_hi = paged_pad(p, (p.causal ? L - p.Nq : (p.window < 0 ? L - 1 : min(L - 1, L - p.Nq + p.window)))) + 1;
     }
 
-    const uint8_t* pK = smem + (n % ST) * C::kStageBytes;
-    const uint8_t* pV = pK + C::kTileBytes;
-    const uint32_t sV = paged_smem(pV);
-    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes);
-    bool some = key0 < free_lo || key0 + TK > free_hi;
-#pragma unroll
-    for (int i = 0; i < TK / 32; ++i) some |= t.valid[i] != 0xffffffffu;
+    const uint8_t* pV = smem + st * C::kStageBytes + C::kTileBytes;
+    const uint32_t kaddr = smem_u32(smem + st * C::kStageBytes) + kat, vaddr = smem_u32(pV) + vat;
+    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes);  // K's, 128 further V's
     // the steps of a tile; kEdge: some row may not see some key of it
     auto steps = [&](auto edge_tile) {
       constexpr bool edge = decltype(edge_tile)::value;
 #pragma unroll 1
     for (int s = 0; s < TK / KW / (16 * KS); ++s) {
       const int kb = (kw * (TK / KW / (16 * KS)) + s) * 16 * KS;
-      uint32_t vm = 0xffffffffu;
-      if (edge) {
-        vm = t.valid[kb >> 5] >> (kb & 31);
-        if ((KS == 2 ? vm : vm & 0xffffu) == 0) continue;  // behind the end
-      }
+      if (edge && kb >= left) break;  // behind the end
       // ---- S^T of keys 16 k + rq (elements 0, 1) and 16 k + rq + 8 (2, 3), rows 2 qd and 2 qd + 1
       float sc[KS][NB][4];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KS; ++k) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) sc[k][nb][0] = sc[k][nb][1] = sc[k][nb][2] = sc[k][nb][3] = 0.f;
+        constexpr int NL = RB / 32;  // 32 bytes of 16 keys a load
+        uint32_t a[NL][4];
 #pragma unroll
-      for (int i = 0; i < (kQuant ? D / 64 : D / 32); ++i)
+        for (int i = 0; i < NL; ++i) ldmatrix_x4(a[i], (kaddr + part(i) + (kb + 16 * k) * PB) ^ ((i << 5) & (PB - 1)));
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint4 a = *reinterpret_cast<const uint4*>(pK + k_at<RB>(kb + 16 * k + rq, qd + 4 * i)),
-                      b = *reinterpret_cast<const uint4*>(pK + k_at<RB>(kb + 16 * k + rq + 8, qd + 4 * i));
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        for (int i = 0; i < NL; ++i) {
           if (kQuant) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int y = 0; y < 2; ++y) {
               uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(aw[x], &a0, &a2);
-              e4m3x4_to_f16(bw[x], &a1, &a3);
+              e4m3x4_to_f16(a[i][2 * y], &a0, &a2);
+              e4m3x4_to_f16(a[i][2 * y + 1], &a1, &a3);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[k][nb], a0, a1, a2, a3, qb[nb][(i * 4 + x) % QS]);
+              for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[k][nb], a0, a1, a2, a3, qb[nb][(2 * i + y) % QS]);
             }
           } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16<false>(sc[k][nb], aw[2 * x], bw[2 * x], aw[2 * x + 1], bw[2 * x + 1], qb[nb][(2 * i + x) % QS]);
+            for (int nb = 0; nb < NB; ++nb) mma16<false>(sc[k][nb], a[i][0], a[i][1], a[i][2], a[i][3], qb[nb][i % QS]);
           }
         }
+      }
       float vs[KS][2];
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float ks = kQuant ? scl[kb + 16 * k + 8 * h + rq] : 1.f;
-          vs[k][h] = kQuant ? scl[TK + kb + 16 * k + 8 * h + rq] : 1.f;
+          vs[k][h] = kQuant ? scl[128 + kb + 16 * k + 8 * h + rq] : 1.f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -539,7 +578,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = 16 * k + rq + 8 * (e >> 1), j = key0 + kb + key;
-              if (((vm >> key) & 1) && j >= rlo[nb][e & 1] && j < rhi[nb][e & 1])
+              if (((boxes >> ((kb + key) >> p.box_log)) & 1) && j >= rlo[nb][e & 1] && j < rhi[nb][e & 1] &&
+                  (p.pad_page == p.c.page_size || paged_slot(p, j) < p.c.page_size))
                 allowed |= 1u << (4 * (k * NB + nb) + e);
               else
                 sc[k][nb][e] = -INFINITY;
@@ -637,17 +677,17 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           uint32_t w[4][D / 32];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int key = kk + 2 * qd + (y & 1) + 8 * (y >> 1);
+            const uint8_t* v = pV + v_at(kk + 2 * qd + (y & 1) + 8 * (y >> 1), rq * (D / 8));
             if (D == 128) {
-              const uint4 v = *reinterpret_cast<const uint4*>(pV + v_at<RB, kQuant>(key, rq));
-              w[y][0] = v.x;
-              w[y][1] = v.y;
-              w[y][2 % (D / 32)] = v.z;
-              w[y][3 % (D / 32)] = v.w;
+              const uint4 x = *reinterpret_cast<const uint4*>(v);
+              w[y][0] = x.x;
+              w[y][1] = x.y;
+              w[y][2 % (D / 32)] = x.z;
+              w[y][3 % (D / 32)] = x.w;
             } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(pV + v_at<RB, kQuant>(key, rq >> 1) + (rq & 1) * 8);
-              w[y][0] = v.x;
-              w[y][1] = v.y;
+              const uint2 x = *reinterpret_cast<const uint2*>(v);
+              w[y][0] = x.x;
+              w[y][1] = x.y;
             }
           }
           if (edge)
@@ -668,13 +708,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
             continue;
           }
         } else {
-          const int key = kk + (lane & 7) + ((lane >> 4) << 3);
-          const uint32_t at = sV + v_at<RB, kQuant>(key, (lane >> 3) & 1);
+          const uint32_t at = vaddr + kk * PB;
           if (edge) {
 #pragma unroll
             for (int x = 0; x < DT; ++x) {
               uint32_t a[4];
-              ldmatrix_x4_trans(a, at ^ (x << 5));
+              ldmatrix_x4_trans(a, (at + part(x)) ^ ((x << 5) & (PB - 1)));
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 bad |= ((a[y] & 0x7f80u) == 0x7f80u) | ((a[y] & 0x7f800000u) == 0x7f800000u);
@@ -685,7 +724,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
             for (int x0 = 0; x0 < DT; x0 += 4) {
               uint32_t a[4][4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], at ^ ((x0 + x) << 5));
+              for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], (at + part(x0 + x)) ^ (((x0 + x) << 5) & (PB - 1)));
 #pragma unroll
               for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -710,16 +749,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int col = dcol(x, e);
-                const uint32_t at = sV + v_at<RB, kQuant>(kk + y, col * ES / 16) + (col * ES) % 16;
-                uint32_t z;
-                float v;
-                if (kQuant) {
-                  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
-                  v = e4m3x2_to_float2(static_cast<uint16_t>(z)).x;
-                } else {
-                  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(z) : "r"(at) : "memory");
-                  v = __uint_as_float(z << 16);
-                }
+                const uint8_t* at = pV + v_at(kk + y, col * ES);
+                const float v = kQuant ? e4m3x2_to_float2(*at).x
+                                       : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) << 16);
                 if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
                 if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
               }
@@ -728,19 +760,22 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     }
 
     };
-    if (some)
+    if (key0 < free_lo || key0 + TK > free_hi || boxes != all_boxes || p.pad_page != p.c.page_size)
       steps(std::true_type{});
     else
       steps(std::false_type{});
 
-    if (!(flags & kFlagSegEnd)) continue;
+    if (!(flags & kFlagSegEnd)) {
+      release();
+      continue;
+    }
     // ---- the segment's end: the KW warps of a row group join their states in tile n's stage
     fresh = true;
     const int b = t.b, unit = t.unit;
     const int kh = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - kh * p.nblk) * C::kRows;
     const bool whole = seg_starts_unit && (flags & kFlagUnitEnd);
     const int slot = 2 * cta + (seg_starts_unit ? 1 : 0);
-    if (n + 1 < cnt) load_q(desc[(n + 1) % kPagedRing]);  // the next unit's queries, on their way meanwhile
+    if (n + 1 < cnt) load_q(t.next_b, t.next_unit);  // the next unit's queries, on their way meanwhile
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -749,10 +784,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
         for (int o = 4; o <= 16; o <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], o);
         if (rq == 0) stat[(warp * NB + nb) * 8 + 2 * qd + c] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
       }
-    float* merge = reinterpret_cast<float*>(smem + (n % ST) * C::kStageBytes);  // [4 warps][8 rows][kMergeStride]
+    float* merge = reinterpret_cast<float*>(smem + st * C::kStageBytes);  // [warps][8 rows][kMergeStride]
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      __syncthreads();  // tile n is read, the block before this one joined
+      if (!join()) return;  // tile n is read, the block before this one joined
       float* mine = merge + (warp * 8 + 2 * qd) * C::kMergeStride;
 #pragma unroll
       for (int x = 0; x < DT; ++x)
@@ -765,8 +800,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
             mine[c * C::kMergeStride + dcol(x, 0)] = acc[nb][x][c];
             mine[c * C::kMergeStride + dcol(x, 1)] = acc[nb][x][2 + c];
           }
-      __syncthreads();
-      constexpr int LPR = D / 4, RPP = kPagedThreads / LPR;  // threads of a row, rows of a pass
+      if (!join()) return;
+      constexpr int LPR = D / 4, RPP = 32 * kPagedWarps / LPR;  // threads of a row, rows of a pass
       const int col = tid % LPR * 4;
 #pragma unroll
       for (int it = 0; it < RG * 8 / RPP; ++it) {
@@ -817,8 +852,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       }
       p.split[cta] = s;
     }
+    fence_proxy_async_smem();  // the stage was written here; the TMA writes it next
+    release();
   }
-  cp_async_wait<0>();
 }
 
 // Joins the partials of the units that several CTAs share: block (c, y) the
