@@ -68,12 +68,15 @@ struct MoveParams {
   long long k_row, k_head, v_row, v_head;  // elements
   const int* cu;                           // [B + 1] offsets of the sequences' rows
   int T;
+  uint32_t row_mul;  // row / (2 * Hkv), as CacheParams::page_mul
+  int row_shift;
 };
 
-// Sequence b with cu[b] <= t < cu[b + 1], or -1: a search by the whole warp, 32
-// offsets a step (two dependent loads for up to 1024 sequences).
-__device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int lane) {
-  int lo = 0, hi = B;  // the answer is the number of b in [0, B) with cu[b + 1] <= t
+// The number of sequences b with cu[b + 1] <= t: the one that t belongs to, if
+// to any.  A search by the whole warp, 32 offsets a step (two dependent loads
+// for up to 1024 sequences).
+__device__ __forceinline__ int first_sequence(const int* cu, int B, int t, int lane) {
+  int lo = 0, hi = B;
   while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + (lane + 1) * step - 1;
@@ -81,105 +84,139 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int la
     lo += __popc(m) * step;
     hi = min(hi, lo + step);
   }
-  const unsigned m = __ballot_sync(0xffffffffu, lo + lane < hi && cu[lo + lane + 1] <= t);
-  const int b = lo + __popc(m);
-  return b < B && cu[b] <= t && t < cu[b + 1] ? b : -1;
+  return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && cu[lo + lane + 1] <= t));
 }
 
-constexpr int kMoveWarps = 8;
-constexpr int kMoveUnroll = 4;  // loads of 512 bytes that a warp has in flight
+// Rows of the dense side in the order token, K then V, head.  Four lanes hold a
+// row (D / 4 values each, 8 at a time, interleaved, so that 4 lanes' loads and
+// stores fill sectors) and a warp 8 * kMoveUnroll rows, which may belong to
+// several tokens.  Few lanes a row keep what a row costs once -- the join of
+// the maximum, two divisions, addresses -- small beside its bytes; a write
+// loads its rows before it looks up where they go.
+constexpr int kMoveWarps = 4;
+constexpr int kMoveUnroll = 2;
+constexpr int kMoveRows = 8 * kMoveUnroll;  // of a warp
 
-// A warp moves kMoveUnroll * 32 / (D / 8) rows of one token (its K and V rows,
-// alternating, head after head); D / 8 lanes hold a row, 16 bytes of bf16 each.
 template <int D, bool kQuant, bool kWrite>
 __global__ void __launch_bounds__(32 * kMoveWarps) cache_move_kernel(const MoveParams p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31;
-  const int chunks = (2 * p.c.Hkv + kRows * kMoveUnroll - 1) / (kRows * kMoveUnroll);
-  const long long task = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(task / chunks);
-  if (t >= p.T) return;
-  const int r0 = static_cast<int>(task % chunks) * kRows * kMoveUnroll + lane / kLanes;
-  const int col = (lane % kLanes) * 8;
+  constexpr int N = D / 32;  // groups of 8 values that a lane holds of a row
+  const int lane = threadIdx.x & 31, q = lane & 3;
+  const uint32_t rows = 2u * p.c.Hkv * p.T;
+  const uint32_t first = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveRows;
+  if (first >= rows) return;
+  auto token_of = [&](uint32_t row) {
+    return static_cast<int>((static_cast<unsigned long long>(row) * p.row_mul) >> (31 + p.row_shift));
+  };
 
-  const int b = find_sequence(p.cu, p.c.B, t, lane);
-  if (b < 0) return;
-  const int pos = cache_length(p.c, b) - (p.cu[b + 1] - t);
-  int slot = 0;
-  const int page = pos >= 0 ? cache_page(p.c, b, pos, &slot) : -1;
-  if (kWrite && page < 0) return;
+  uint4 x[kMoveUnroll][N];
+  int token[kMoveUnroll], head[kMoveUnroll];
+  bool isv[kMoveUnroll], on[kMoveUnroll];
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    const uint32_t row = first + 8 * u + (lane >> 2);
+    on[u] = row < rows;
+    token[u] = token_of(on[u] ? row : first);
+    const int h = static_cast<int>((on[u] ? row : first) - 2u * p.c.Hkv * token[u]);
+    isv[u] = h >= p.c.Hkv;
+    head[u] = isv[u] ? h - p.c.Hkv : h;
+  }
+  auto dense = [&](int u) {
+    return (isv[u] ? p.v + 2 * (token[u] * p.v_row + head[u] * p.v_head) : p.k + 2 * (token[u] * p.k_row + head[u] * p.k_head)) +
+           q * 16;
+  };
+  if (kWrite) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const uint8_t* src = dense(u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(src + i * 64));
+    }
+  }
 
-  uint4 x[kMoveUnroll];
+  // ---- where the rows live: the sequence of the warp's first token, from which each lane goes on to its own
+  const int t0 = token_of(first);
+  const int b0 = first_sequence(p.cu, p.c.B, t0, lane);
+  int page[kMoveUnroll], slot[kMoveUnroll];
+#pragma unroll
+  for (int u = 0; u < kMoveUnroll; ++u) {
+    int b = b0;
+    while (b < p.c.B && p.cu[b + 1] <= token[u]) ++b;
+    on[u] = on[u] && b < p.c.B && p.cu[b] <= token[u];
+    page[u] = -1;
+    slot[u] = 0;
+    if (on[u]) {
+      const int pos = cache_length(p.c, b) - (p.cu[b + 1] - token[u]);
+      if (pos >= 0) page[u] = cache_page(p.c, b, pos, &slot[u]);
+    }
+    if (kWrite) on[u] = on[u] && page[u] >= 0;
+  }
+
   float sc[kMoveUnroll];
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {
-    const int r = r0 + u * kRows, h = r >> 1;
-    x[u] = make_uint4(0, 0, 0, 0);
     sc[u] = 0.f;
-    if (h >= p.c.Hkv) continue;
-    if (kWrite) {
-      const uint8_t* src = (r & 1) ? p.v : p.k;
-      const long long at = (r & 1) ? t * p.v_row + h * p.v_head : t * p.k_row + h * p.k_head;
-      x[u] = __ldg(reinterpret_cast<const uint4*>(src + (at + col) * 2));
-    } else if (page >= 0) {
-      const uint8_t* src = (r & 1) ? p.c.v : p.c.k;
-      const long long at = p.c.pages.row(page, h, slot) + col;
+    if (kWrite) continue;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
+    if (!on[u] || page[u] < 0) continue;  // a place without a page reads as zero
+    const uint8_t* src = (isv[u] ? p.c.v : p.c.k) + p.c.pages.row(page[u], head[u], slot[u]) * (kQuant ? 1 : 2);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
       if (kQuant) {
-        const uint2 w = *reinterpret_cast<const uint2*>(src + at);
-        x[u].x = w.x;
-        x[u].y = w.y;
-        sc[u] = ((r & 1) ? p.c.vs : p.c.ks)[p.c.scales.row(page, h, slot)];
+        const uint2 w = *reinterpret_cast<const uint2*>(src + q * 8 + i * 32);
+        x[u][i].x = w.x;
+        x[u][i].y = w.y;
       } else {
-        x[u] = *reinterpret_cast<const uint4*>(src + at * 2);
+        x[u][i] = *reinterpret_cast<const uint4*>(src + q * 16 + i * 64);
       }
-    }
+    if (kQuant) sc[u] = (isv[u] ? p.c.vs : p.c.ks)[p.c.scales.row(page[u], head[u], slot[u])];
   }
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {
-    const int r = r0 + u * kRows, h = r >> 1;
     if (kWrite && kQuant) {
       // |x| as integers: NaN > infinity > finite, so one maximum finds both
-      uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
-                            __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
-      m = max(m & 0xffffu, m >> 16);
+      uint32_t m = 0;
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int i = 0; i < N; ++i)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[u][i].x & 0x7fff7fffu, x[u][i].y & 0x7fff7fffu),
+                                 __vmaxu2(x[u][i].z & 0x7fff7fffu, x[u][i].w & 0x7fff7fffu)));
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      if (!on[u]) continue;
       const float amax = m > 0x7f80u ? __uint_as_float(0x7fc00000u)
                                      : fminf(fmaxf(__uint_as_float(m << 16), kAmaxLo), FLT_MAX);
       const float inv = __fdiv_rn(kE4m3Max, amax);
-      if (h >= p.c.Hkv) continue;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint16_t code[4];
+      uint8_t* dst = (isv[u] ? p.c.v : p.c.k) + p.c.pages.row(page[u], head[u], slot[u]) + q * 8;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        code[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w[i] << 16) * inv,
-                                                       __uint_as_float(w[i] & 0xffff0000u) * inv),
-                                           __NV_SATFINITE, __NV_E4M3);
-      const uint2 out = make_uint2(code[0] | (static_cast<uint32_t>(code[1]) << 16),
-                                   code[2] | (static_cast<uint32_t>(code[3]) << 16));
-      uint8_t* dst = (r & 1) ? p.c.v : p.c.k;
-      *reinterpret_cast<uint2*>(dst + p.c.pages.row(page, h, slot) + col) = out;
-      if (col == 0) ((r & 1) ? p.c.vs : p.c.ks)[p.c.scales.row(page, h, slot)] = __fdiv_rn(amax, kE4m3Max);
-    } else if (h < p.c.Hkv) {
-      if (kWrite) {
-        uint8_t* dst = (r & 1) ? p.c.v : p.c.k;
-        *reinterpret_cast<uint4*>(dst + (p.c.pages.row(page, h, slot) + col) * 2) = x[u];
-      } else {
+      for (int i = 0; i < N; ++i) {
+        const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+        uint16_t code[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          code[y] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w[y] << 16) * inv,
+                                                         __uint_as_float(w[y] & 0xffff0000u) * inv),
+                                             __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2*>(dst + i * 32) = make_uint2(code[0] | (static_cast<uint32_t>(code[1]) << 16),
+                                                             code[2] | (static_cast<uint32_t>(code[3]) << 16));
+      }
+      if (q == 0) (isv[u] ? p.c.vs : p.c.ks)[p.c.scales.row(page[u], head[u], slot[u])] = __fdiv_rn(amax, kE4m3Max);
+    } else if (on[u]) {
+      uint8_t* dst = kWrite ? (isv[u] ? p.c.v : p.c.k) + 2 * p.c.pages.row(page[u], head[u], slot[u]) + q * 16 : dense(u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
         if (kQuant) {
-          const uint32_t w[2] = {x[u].x, x[u].y};
+          const uint32_t w[2] = {x[u][i].x, x[u][i].y};
           uint32_t out[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
-            const __nv_bfloat162 y = __floats2bfloat162_rn(f.x * sc[u], f.y * sc[u]);
-            out[i] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(w[y >> 1] >> (16 * (y & 1))));
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * sc[u], f.y * sc[u]);
+            out[y] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          // a place without a page reads as zero, whatever 0 * 0 above
-          x[u] = make_uint4(out[0], out[1], out[2], out[3]);
+          x[u][i] = make_uint4(out[0], out[1], out[2], out[3]);
         }
-        uint8_t* dst = (r & 1) ? p.v : p.k;
-        const long long at = (r & 1) ? t * p.v_row + h * p.v_head : t * p.k_row + h * p.k_head;
-        *reinterpret_cast<uint4*>(dst + (at + col) * 2) = x[u];
+        *reinterpret_cast<uint4*>(dst + i * 64) = x[u][i];
       }
     }
   }

@@ -149,10 +149,11 @@ fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_st
   p.v_head = sv.h;
   p.cu = cu;
   p.T = T;
-  const int rows = 256 / d * fa::kMoveUnroll;  // rows a warp moves
-  const long long tasks = static_cast<long long>(T) * ((2LL * Hkv + rows - 1) / rows);
-  const long long blocks = (tasks + fa::kMoveWarps - 1) / fa::kMoveWarps;
-  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const long long rows = 2LL * Hkv * T;
+  if (rows > (1LL << 31) - fa::kMoveWarps * fa::kMoveRows) return FA_ERR_UNSUPPORTED;  // counted in 32 bits
+  if (Hkv > (1 << 29)) return FA_ERR_UNSUPPORTED;
+  magic(2 * Hkv, &p.row_mul, &p.row_shift);
+  const long long blocks = (rows + fa::kMoveWarps * fa::kMoveRows - 1) / (fa::kMoveWarps * fa::kMoveRows);
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * fa::kMoveWarps);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = cache->dtype == FA_CACHE_E4M3;
@@ -242,8 +243,8 @@ template <int D, bool kQuant>
 fa_status launch_paged_rows(const fa::PagedParams& p, const CUtensorMap* maps, double tiles, cudaStream_t st) {
   switch (paged_rows(p.R)) {
     case 8: return launch_paged<D, kQuant, 1, 1>(p, maps, tiles, st);
-    case 16: return launch_paged<D, kQuant, 2, 1>(p, maps, tiles, st);
-    case 32: return launch_paged<D, kQuant, 2, 2>(p, maps, tiles, st);
+    case 16: return launch_paged<D, kQuant, 1, 2>(p, maps, tiles, st);
+    case 32: return launch_paged<D, kQuant, 1, 4>(p, maps, tiles, st);
     default: return launch_paged<D, kQuant, 2, 4>(p, maps, tiles, st);
   }
 }

@@ -82,7 +82,7 @@ struct PagedCfg {
   static constexpr int kStatBytes = kPagedWarps * 8 * NB * 16;
   static constexpr int kSmemBytes = kStages * (kStageBytes + 16 + 48) + kStatBytes + 16 + 128;
   static_assert(kStages >= 2, "a tile loads while another is computed");
-  static_assert(kPagedWarps * 8 * kMergeStride * 4 <= 2 * kTileBytes, "the warps' accumulators are joined in a stage");
+  static_assert(kPagedWarps * 8 * kMergeStride * 4 <= kStageBytes, "the warps' accumulators are joined in a stage");
 };
 
 // 4 bytes to shared memory, zero when !on.
@@ -369,29 +369,42 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
         mbar_arrive_expect_tx(full + st, (live << p.box_log) * 2 * RB);
       }
       const int page = on ? cur.page : p.c.num_pages;
-      for (int i = 0; i < live; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, i), slot = __shfl_sync(0xffffffffu, cur.slot, i);
-        if (lane == 0) {
-          uint8_t* to = dst + (i << p.box_log) * PB;
+      for (int i0 = 0; i0 < live; i0 += 4) {
+        int pg[4], slot[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pg[i] = __shfl_sync(0xffffffffu, page, i0 + i);
+          slot[i] = __shfl_sync(0xffffffffu, cur.slot, i0 + i);
+        }
+        if (lane != 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i0 + i >= live) break;
+          uint8_t* to = dst + ((i0 + i) << p.box_log) * PB;
 #pragma unroll
           for (int h = 0; h < RB / PB; ++h) {
-            tma_load_4d(&map_k, full + st, to + h * TK * PB, h * PB / ES, slot, kh, pg);
-            tma_load_4d(&map_v, full + st, to + h * TK * PB + C::kTileBytes, h * PB / ES, slot, kh, pg);
+            tma_load_4d(&map_k, full + st, to + h * TK * PB, h * PB / ES, slot[i], kh, pg[i]);
+            tma_load_4d(&map_v, full + st, to + h * TK * PB + C::kTileBytes, h * PB / ES, slot[i], kh, pg[i]);
           }
         }
       }
       if (kQuant) {
         const long long at = on ? p.c.scales.row(cur.page, kh, cur.slot) : -1;
-        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes);
+        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes) + lane * 4;
+        long long off[TK / 32];
+        bool here[TK / 32];
 #pragma unroll
-        for (int r = lane; r < TK; r += 32) {
-          const int src = r >> p.box_log, in = r & (box - 1);
-          long long off = __shfl_sync(0xffffffffu, at, src);
+        for (int i = 0; i < TK / 32; ++i) {
+          const int src = (i * 32 + lane) >> p.box_log, in = lane & (box - 1);
+          off[i] = __shfl_sync(0xffffffffu, at, src);
           const int slot = __shfl_sync(0xffffffffu, cur.slot, src) + in;
-          const bool here = off >= 0 && slot < p.c.page_size;
-          off = here ? off + in * p.c.scales.n : 0;
-          cp_async4(to + r * 4, p.c.ks + off, here);
-          cp_async4(to + 512 + r * 4, p.c.vs + off, here);
+          here[i] = off[i] >= 0 && slot < p.c.page_size;
+          off[i] += in * p.c.scales.n;
+        }
+#pragma unroll
+        for (int i = 0; i < TK / 32; ++i) {
+          cp_async4(to + i * 128, p.c.ks + (here[i] ? off[i] : 0), here[i]);
+          cp_async4(to + i * 128 + 512, p.c.vs + (here[i] ? off[i] : 0), here[i]);
         }
         cp_async_arrive(full + st);
       }

@@ -288,7 +288,7 @@ typedef struct {
  * of sequence b: with n_b of them, row cu[b] + i is position seqlens[b] - n_b +
  * i, so seqlens counts the tokens of this call.  Rows whose position is
  * negative are not written, and read back as zero; rows outside [cu[0], cu[B])
- * are not read, and left as they are.  Everything but these rows' places in the
+ * go nowhere, and are left as they are.  Everything but these rows' places in the
  * cache stays as it was.  Two rows of one call must not share a place (two
  * sequences with the same page): which one it then holds is not defined.
  * fa_cache_read writes k and v, whose layout must be one-to-one as for an output
