@@ -9,9 +9,11 @@ CPU fallback: if the library is missing or a call fails, an error is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
+import struct
 
 __all__ = ["lib", "FAError", "FA_BF16", "FA_FP32", "fwd", "bwd", "bwd_workspace_size", "device_status",
            "exported_names", "set_timing_events", "bwd_noalloc", "fwd_splitkv", "fwd_blocksparse", "bwd_blocksparse", "fwd_varlen", "bwd_varlen", "fwd_strided", "bwd_strided",
@@ -589,10 +591,17 @@ class _PagedCache(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+# The same two structures packed without ctypes objects: these calls are short
+# next to what their arguments cost to describe.
+_pack_cache = struct.Struct("6Q7q7i4x").pack  # _PagedCache
+_pack_two = struct.Struct("6q").pack          # _Strides * 2
+assert struct.calcsize("6Q7q7i4x") == ctypes.sizeof(_PagedCache)
+
+
 def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
-    """Checks a paged cache's tensors against each other; the _PagedCache that
-    describes them (it holds pointers only: the tensors stay the caller's) and
-    their device."""
+    """Checks a paged cache's tensors against each other; the fa_paged_cache that
+    describes them (it holds pointers only: the tensors stay the caller's), their
+    device, and the numbers of sequences, kv heads and head_dim."""
     import torch
     if k_pages.dim() != 4:
         raise ValueError("k_pages, v_pages must be 4-D [pages, kv heads, page size, head_dim]")
@@ -620,7 +629,7 @@ def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
     if (M > 1 and table_stride[1] != 1) or (B > 1 and (table_stride[0] < M or seqlens.stride(0) != 1)):
         raise ValueError("page_table must have contiguous rows that do not overlap, and seqlens must be contiguous")
     tensors = [(v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens")]
-    ks = vs = ss = None
+    ks = vs = s0 = s1 = s2 = 0
     if code == FA_CACHE_BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale, v_scale belong to a float8_e4m3fn cache")
@@ -628,7 +637,7 @@ def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is None or t.shape != shape[:3] or t.dtype != torch.float32:
                 raise ValueError(f"{name}: must be a float32 tensor of shape {tuple(shape[:3])}")
-        ss = k_scale.stride()
+        s0, s1, s2 = ss = k_scale.stride()
         if v_scale.stride() != ss:
             raise ValueError("k_scale, v_scale must have the same strides")
         tensors += [(k_scale, "k_scale"), (v_scale, "v_scale")]
@@ -639,30 +648,28 @@ def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
     for t, name in tensors:
         if t.get_device() != at:
             raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {k_pages.device})")
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, page_table.data_ptr(), seqlens.data_ptr(),
-                       st[:3], ss or (0, 0, 0), table_stride[0], B, Hkv, d, P, page, M, code), k_pages.device
+    return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, page_table.data_ptr(), seqlens.data_ptr(), st[0],
+                       st[1], st[2], s0, s1, s2, table_stride[0], B, Hkv, d, P, page, M, code), k_pages.device, B, Hkv, d
 
 
-def _move_args(c, k, v, cu_seqlens, T, device):
+def _move_args(B, Hkv, d, k, v, cu_seqlens, T, device):
     """Checks the packed tokens k, v [T, Hkv, d] (d contiguous) and the device
-    offsets of cache_write() / cache_read(); their fa_strides."""
+    offsets of cache_write() / cache_read(); their two fa_strides."""
     import torch
-    shape, at, strides = (T, c.Hkv, c.d), device.index, []
+    shape, at = (T, Hkv, d), device.index
     for t, name in ((k, "k"), (v, "v")):
         if t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
-        st = t.stride()
-        if st[2] != 1:
+        if t.stride(2) != 1:
             raise ValueError(f"{name}: must have a contiguous last axis")
         if t.get_device() != at:
             raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {device})")
-        strides.append((1, st[1], st[0]))
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (c.B + 1,) or cu_seqlens.get_device() != at \
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (B + 1,) or cu_seqlens.get_device() != at \
             or cu_seqlens.stride(0) != 1:
-        raise TypeError(f"cu_seqlens must be a contiguous int32 tensor of {c.B + 1} values on the device of k_pages")
-    return (_Strides * 2)(*strides)
+        raise TypeError(f"cu_seqlens must be a contiguous int32 tensor of {B + 1} values on the device of k_pages")
+    return _pack_two(1, k.stride(1), k.stride(0), 1, v.stride(1), v.stride(0))
 
 
 def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale=None, v_scale=None):
@@ -673,12 +680,12 @@ def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale
     scale per token and kv head in k_scale, v_scale [P,Hkv,page] float32,
     float8_e4m3fn; page_table [B,pages of a sequence], cu_seqlens and seqlens
     int32, all on one CUDA device."""
-    c, device = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    c, device, B, Hkv, d = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
     T = k.shape[0]
-    st = _move_args(c, k, v, cu_seqlens, T, device)
+    st = _move_args(B, Hkv, d, k, v, cu_seqlens, T, device)
     if T == 0:
         return
-    code = _on(device, lib().fa_cache_write, ctypes.addressof(c), k.data_ptr(), v.data_ptr(), ctypes.addressof(st),
+    code = _on(device, lib().fa_cache_write, c, k.data_ptr(), v.data_ptr(), st,
                cu_seqlens.data_ptr(), T, FA_BF16, _stream_ptr(device))
     _check(code, "fa_cache_write")
 
@@ -691,22 +698,23 @@ def cache_read(k_pages, v_pages, page_table, cu_seqlens, seqlens, num_tokens: in
     any token and head strides; its rows outside the offsets are left as they
     were (uninitialised when allocated here)."""
     import torch
-    c, device = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    c, device, B, Hkv, d = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
     T = int(num_tokens)
     if out is None:
-        k = torch.empty((T, c.Hkv, c.d), dtype=torch.bfloat16, device=device)
+        k = torch.empty(T, Hkv, d, dtype=torch.bfloat16, device=device)
         v = torch.empty_like(k)
     else:
         k, v = out
-    st = _move_args(c, k, v, cu_seqlens, T, device)
+    st = _move_args(B, Hkv, d, k, v, cu_seqlens, T, device)
     if T == 0:
         return k, v
-    code = _on(device, lib().fa_cache_read, ctypes.addressof(c), k.data_ptr(), v.data_ptr(), ctypes.addressof(st),
+    code = _on(device, lib().fa_cache_read, c, k.data_ptr(), v.data_ptr(), st,
                cu_seqlens.data_ptr(), T, FA_BF16, _stream_ptr(device))
     _check(code, "fa_cache_read")
     return k, v
 
 
+@functools.lru_cache(maxsize=64)
 def fwd_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
     return int(lib().fa_fwd_paged_workspace_size(B, H, Hkv, Nq, d))
 
@@ -718,29 +726,30 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
     values already: fwd_decode() for sequences of different lengths (see
     fa_fwd_paged in fa.h; the cache's tensors are those of cache_write())."""
     import torch
-    c, device = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
-    if q.dim() != 4:
+    c, device, B, Hkv, d = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be 4-D [batch, heads, rows, head_dim]")
-    B, H, Nq, d = q.shape
-    if B != c.B or d != c.d:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected {c.B} sequences of head_dim {c.d}")
+    _, H, Nq, _ = shape
+    if shape[0] != B or shape[3] != d:
+        raise ValueError(f"q: shape {tuple(shape)}, expected {B} sequences of head_dim {d}")
     if q.dtype != torch.bfloat16:
         raise TypeError(f"q: dtype {q.dtype}, expected torch.bfloat16")
     if q.get_device() != device.index:
         raise ValueError(f"q: must be on the CUDA device of k_pages, got {q.device} (k_pages: {device})")
     if out is not None:
-        _same(out, q.shape, q, "out", contiguous=False)
+        _same(out, shape, q, "out", contiguous=False)
     if lse is not None:
         _check_lse(lse, (B, H, Nq), q)
     if workspace is not None:
         _check_workspace(workspace, device)
     dense = q.is_contiguous()
-    o = (torch.empty_like(q) if dense else q.new_empty((B, H, Nq, d))) if out is None else out
-    l = torch.empty((B, H, Nq), dtype=torch.float32, device=device) if lse is None else lse
+    o = (torch.empty_like(q) if dense else q.new_empty(shape)) if out is None else out
+    l = torch.empty(B, H, Nq, dtype=torch.float32, device=device) if lse is None else lse
     st = None if dense and (out is None or out.is_contiguous()) else _strides_of(q, o)
-    ws = torch.empty(max(fwd_paged_workspace_size(B, H, c.Hkv, Nq, d), 16), dtype=torch.uint8, device=device) \
+    ws = torch.empty(max(fwd_paged_workspace_size(B, H, Hkv, Nq, d), 16), dtype=torch.uint8, device=device) \
         if workspace is None else workspace
-    code = _on(device, lib().fa_fwd_paged, ctypes.addressof(c), q.data_ptr(), o.data_ptr(), l.data_ptr(),
+    code = _on(device, lib().fa_fwd_paged, c, q.data_ptr(), o.data_ptr(), l.data_ptr(),
                None if st is None else ctypes.addressof(st), H, Nq, 1.0 / math.sqrt(d) if scale is None else float(scale),
                int(bool(causal)), int(window), ws.data_ptr(), ws.numel(), FA_BF16, _stream_ptr(device))
     _check(code, "fa_fwd_paged")
