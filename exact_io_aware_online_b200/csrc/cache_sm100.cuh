@@ -155,21 +155,22 @@ __global__ void __launch_bounds__(32 * kMoveWarps) cache_move_kernel(const MoveP
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {
     sc[u] = 0.f;
-    if (kWrite) continue;
+    if (!kWrite) {
+      const bool there = on[u] && page[u] >= 0;  // a place without a page reads as zero
+      const uint8_t* src = there ? (isv[u] ? p.c.v : p.c.k) + p.c.pages.row(page[u], head[u], slot[u]) * (kQuant ? 1 : 2) : p.c.k;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[u][i] = make_uint4(0, 0, 0, 0);
-    if (!on[u] || page[u] < 0) continue;  // a place without a page reads as zero
-    const uint8_t* src = (isv[u] ? p.c.v : p.c.k) + p.c.pages.row(page[u], head[u], slot[u]) * (kQuant ? 1 : 2);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (kQuant) {
-        const uint2 w = *reinterpret_cast<const uint2*>(src + q * 8 + i * 32);
-        x[u][i].x = w.x;
-        x[u][i].y = w.y;
-      } else {
-        x[u][i] = *reinterpret_cast<const uint4*>(src + q * 16 + i * 64);
+      for (int i = 0; i < N; ++i) {
+        x[u][i] = make_uint4(0, 0, 0, 0);
+        if (there && kQuant) {
+          const uint2 w = *reinterpret_cast<const uint2*>(src + q * 8 + i * 32);
+          x[u][i].x = w.x;
+          x[u][i].y = w.y;
+        } else if (there) {
+          x[u][i] = *reinterpret_cast<const uint4*>(src + q * 16 + i * 64);
+        }
       }
-    if (kQuant) sc[u] = (isv[u] ? p.c.vs : p.c.ks)[p.c.scales.row(page[u], head[u], slot[u])];
+      if (kQuant && there) sc[u] = (isv[u] ? p.c.vs : p.c.ks)[p.c.scales.row(page[u], head[u], slot[u])];
+    }
   }
 #pragma unroll
   for (int u = 0; u < kMoveUnroll; ++u) {

@@ -212,14 +212,23 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   // ---- this group's share [s0, s1) of the list, in which a unit counts its tiles and c0
   auto tiles_of = [&](int b) { return b < B ? paged_tiles<TK>(p, cache_length(p.c, b)) : 0; };
   auto packed = [](int nt) { return (static_cast<long long>(nt) << 32) + (nt != 0); };  // tiles, sequences with keys
-  long long sum = 0;
-  for (int b = tid; b < B; b += kPagedThreads) sum += packed(tiles_of(b));
+  const int per = (B + kPagedThreads - 1) / kPagedThreads;  // sequences of a thread: per * tid ...
+  long long mine = 0, incl, sum = 0;
+  for (int i = 0; i < per; ++i) mine += packed(tiles_of(per * tid + i));
+  incl = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[warp] = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) red[warp] = incl;
   __syncthreads();
-  sum = 0;
-  for (int w = 0; w < kPagedThreads / 32; ++w) sum += red[w];
+  long long before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kPagedThreads / 32; ++w) {
+    if (w < warp) before += red[w];
+    sum += red[w];
+  }
   const int c0 = (sum >> 32) * U >= 2LL * groups ? 1 : 0;  // few tiles: one for each CTA
   auto cost = [&](long long x) { return ((x >> 32) + (x & 0xffffffffLL) * c0) * U; };
   const long long W = cost(sum);
@@ -246,53 +255,39 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   // ---- the front cursor: sequence, unit and tile of s0; the tiles up to s1
   int fb, fu, ft, cnt;
   long long last_end;  // where the unit that s1 lies in ends
-  {
-    long long base = 0;
-    __syncthreads();
-    if (tid == 0) red[12] = (sum >> 32) * U, red[13] = W;  // s1 at the very end
-    for (int at = 0;; at += kPagedThreads) {
-      const int b = at + tid, nt = tiles_of(b);
-      long long incl = packed(nt);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const long long at = e ? s1 : s0;
+    if (e && tid == 0 && s1 == W) red[12] = (sum >> 32) * U, red[13] = W;
+    if (at < cost(before) || at >= cost(before + mine)) continue;
+    long long from = before;
+    for (int b = per * tid;; ++b) {  // found before this thread's sequences end
+      const int nt = tiles_of(b);
+      if (at >= cost(from + packed(nt))) {
+        from += packed(nt);
+        continue;
       }
-      __syncthreads();
-      if (lane == 31) red[warp] = incl;
-      __syncthreads();
-      long long before = base;
-      for (int w = 0; w < warp; ++w) before += red[w];
-      const long long first = before + incl - packed(nt), lo = cost(first), hi = cost(before + incl);
-      if (nt != 0) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const long long at_s = e ? s1 : s0;
-          if (lo > at_s || at_s >= hi) continue;
-          const int u = static_cast<int>((at_s - lo) / (nt + c0)), off = static_cast<int>((at_s - lo) % (nt + c0));
-          const int t = max(0, off - c0);
-          const long long done = (first >> 32) * U + static_cast<long long>(u) * nt + t;  // tiles before it
-          if (e) {
-            red[12] = done;
-            red[13] = at_s - off + nt + c0;
-          } else {
-            red[8] = b;
-            red[9] = u;
-            red[10] = t;
-            red[11] = done;
-          }
-        }
+      const long long in = at - cost(from);
+      const int u = static_cast<int>(in / (nt + c0)), off = static_cast<int>(in % (nt + c0)), t = max(0, off - c0);
+      const long long done = (from >> 32) * U + static_cast<long long>(u) * nt + t;  // tiles before it
+      if (e) {
+        red[12] = done;
+        red[13] = at - off + nt + c0;
+      } else {
+        red[8] = b;
+        red[9] = u;
+        red[10] = t;
+        red[11] = done;
       }
-      for (int w = 0; w < kPagedThreads / 32; ++w) base += red[w];
-      if (s1 < cost(base) || at + kPagedThreads >= B) break;  // found (uniform)
+      break;
     }
-    __syncthreads();
-    fb = static_cast<int>(red[8]);
-    fu = static_cast<int>(red[9]);
-    ft = static_cast<int>(red[10]);
-    cnt = static_cast<int>(red[12] - red[11]);
-    last_end = red[13];
   }
+  __syncthreads();
+  fb = static_cast<int>(red[8]);
+  fu = static_cast<int>(red[9]);
+  ft = static_cast<int>(red[10]);
+  cnt = static_cast<int>(red[12] - red[11]);
+  last_end = red[13];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == kPagedWarps) {
@@ -584,19 +579,29 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       uint32_t allowed = 0xffffffffu;  // bit 4 (k NB + nb) + e
       if (edge) {
         allowed = 0;
+        const int j0 = key0 + kb + rq;
+        bool here[KS][2];  // key 16 k + 8 h + rq exists (8 keys in line are in one box)
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int h = 0; h < 2; ++h) {
+            here[k][h] = (boxes >> ((kb + 16 * k + 8 * h) >> p.box_log)) & 1;
+            if (p.pad_page != p.c.page_size) here[k][h] &= paged_slot(p, j0 + 16 * k + 8 * h) < p.c.page_size;
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = 16 * k + rq + 8 * (e >> 1), j = key0 + kb + key;
-              if (((boxes >> ((kb + key) >> p.box_log)) & 1) && j >= rlo[nb][e & 1] && j < rhi[nb][e & 1] &&
-                  (p.pad_page == p.c.page_size || paged_slot(p, j) < p.c.page_size))
-                allowed |= 1u << (4 * (k * NB + nb) + e);
-              else
-                sc[k][nb][e] = -INFINITY;
-            }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int lo = rlo[nb][c] - j0, hi = rhi[nb][c] - j0;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (here[k][h] && 16 * k + 8 * h >= lo && 16 * k + 8 * h < hi)
+                  allowed |= 1u << (4 * (k * NB + nb) + 2 * h + c);
+                else
+                  sc[k][nb][2 * h + c] = -INFINITY;
+          }
       }
       auto on = [&](int k, int nb, int e) { return !edge || ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
       // ---- running maximum: moved only when it grows by more than 8 (weights
@@ -681,11 +686,34 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
                                                : pack_bf16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1]));
         }
       }
+      // The slow form of columns dcol(x0 .. x0 + 3, .): products one by one in
+      // fp32, weights of zero left out.  For an infinity or NaN among the values
+      // of a tile that some rows see only in part (0 * infinity would reach rows
+      // that may not see that key), and for value scales too far apart for f16.
+      auto one_by_one = [&](int k, int x0) {
+#pragma unroll 1
+        for (int y = 0; y < 16; ++y)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int src = (y & 7) * 4 + qd;
+            const float f0 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][0] : sc[k][nb][2], src);
+            const float f1 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][1] : sc[k][nb][3], src);
+#pragma unroll
+            for (int x = x0; x < x0 + 4; ++x)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint8_t* at = pV + v_at(kb + 16 * k + y, dcol(x, e) * ES);
+                const float v = kQuant ? e4m3x2_to_float2(*at).x
+                                       : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) << 16);
+                if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
+                if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
+              }
+          }
+      };
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int kk = kb + 16 * k;
-        uint32_t bad = slow[k];
         if (kQuant) {
           uint32_t w[4][D / 32];
 #pragma unroll
@@ -703,12 +731,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
               w[y][1] = x.y;
             }
           }
-          if (edge)
+          uint32_t bad = 0;
+          if (edge) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)
 #pragma unroll
-              for (int z = 0; z < D / 32; ++z) bad |= ((w[y][z] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // NaN codes
-          if (!__any_sync(0xffffffffu, bad)) {
+              for (int z = 0; z < D / 32; ++z) bad |= (w[y][z] & 0x7f7f7f7fu) + 0x01010101u;
+            bad &= 0x80808080u;  // a NaN's code
+          }
+          if (!__any_sync(0xffffffffu, slow[k] || bad)) {
 #pragma unroll
             for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
               const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
@@ -718,57 +749,34 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[k][nb]);
             }
-            continue;
+          } else {
+#pragma unroll
+            for (int x0 = 0; x0 < DT; x0 += 4) one_by_one(k, x0);
           }
         } else {
           const uint32_t at = vaddr + kk * PB;
-          if (edge) {
 #pragma unroll
-            for (int x = 0; x < DT; ++x) {
-              uint32_t a[4];
-              ldmatrix_x4_trans(a, (at + part(x)) ^ ((x << 5) & (PB - 1)));
+          for (int x0 = 0; x0 < DT; x0 += 4) {
+            uint32_t a[4][4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                bad |= ((a[y] & 0x7f80u) == 0x7f80u) | ((a[y] & 0x7f800000u) == 0x7f800000u);
+            for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], (at + part(x0 + x)) ^ (((x0 + x) << 5) & (PB - 1)));
+            bool bad = false;
+            if (edge) {  // value * 0 is a zero for finite values, NaN for others
+              __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f), t = z;
+#pragma unroll
+              for (int x = 0; x < 16; ++x) t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a[x >> 2][x & 3]), z, t);
+              bad = (*reinterpret_cast<const uint32_t*>(&t) & 0x7fff7fffu) != 0;
             }
-          }
-          if (!edge || !__any_sync(0xffffffffu, bad)) {
-#pragma unroll
-            for (int x0 = 0; x0 < DT; x0 += 4) {
-              uint32_t a[4][4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], (at + part(x0 + x)) ^ (((x0 + x) << 5) & (PB - 1)));
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x0 + x], a[x][0], a[x][1], a[x][2], a[x][3], pb[k][nb]);
+            if (edge && __any_sync(0xffffffffu, bad)) {
+              one_by_one(k, x0);
+              continue;
             }
-            continue;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x0 + x], a[x][0], a[x][1], a[x][2], a[x][3], pb[k][nb]);
           }
         }
-        // The slow form: products one by one in fp32, weights of zero left out.
-        // For an infinity or NaN among the values of a tile that some rows see
-        // only in part (0 * infinity would reach rows that may not see that key),
-        // and for value scales too far apart for f16.
-#pragma unroll 1
-        for (int y = 0; y < 16; ++y)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const int src = (y & 7) * 4 + qd;
-            const float f0 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][0] : sc[k][nb][2], src);
-            const float f1 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][1] : sc[k][nb][3], src);
-#pragma unroll
-            for (int x = 0; x < DT; ++x)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int col = dcol(x, e);
-                const uint8_t* at = pV + v_at(kk + y, col * ES);
-                const float v = kQuant ? e4m3x2_to_float2(*at).x
-                                       : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) << 16);
-                if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
-                if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
-              }
-          }
       }
     }
 
@@ -803,9 +811,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       if (!join()) return;  // tile n is read, the block before this one joined
       float* mine = merge + (warp * 8 + 2 * qd) * C::kMergeStride;
 #pragma unroll
-      for (int x = 0; x < DT; ++x)
+      for (int c = 0; c < 2; ++c) {
+        if (row0 + (rg * NB + nb) * 8 + 2 * qd + c >= p.R) continue;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int x = 0; x < DT; ++x)
           if (kQuant) {
             *reinterpret_cast<float2*>(mine + c * C::kMergeStride + dcol(x, 0)) =
                 make_float2(acc[nb][x][c], acc[nb][x][2 + c]);
@@ -813,6 +822,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
             mine[c * C::kMergeStride + dcol(x, 0)] = acc[nb][x][c];
             mine[c * C::kMergeStride + dcol(x, 1)] = acc[nb][x][2 + c];
           }
+      }
       if (!join()) return;
       constexpr int LPR = D / 4, RPP = 32 * kPagedWarps / LPR;  // threads of a row, rows of a pass
       const int col = tid % LPR * 4;
@@ -890,7 +900,24 @@ __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(c
   float m = -INFINITY, l = 0.f, u = 0x1p-126f, acc[E];  // u: the accumulators' unit, the largest so far
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  constexpr int kAhead = 8;
+  float v[kAhead][E];
+  auto load = [&](int i, int cnt) {
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const float* src = p.part_o + at(i + y) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float2 f = make_float2(0.f, 0.f);
+        if (y < cnt) f = *reinterpret_cast<const float2*>(src + e);
+        v[y][e] = f.x;
+        v[y][e + 1] = f.y;
+      }
+    }
+  };
   for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int cnt = min(32, parts - i0);
+    load(i0, cnt);  // on their way while the weights are formed
     float4 st = make_float4(-INFINITY, 0.f, 0x1p-126f, 0.f);
     if (i0 + lane < parts) st = p.part_m[at(i0 + lane)];
     float mn = fmaxf(m, st.x), un = fmaxf(u, st.z);
@@ -912,26 +939,15 @@ __global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(c
     u = un;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= old;
-    const int cnt = min(32, parts - i0);
-#pragma unroll 8
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.part_o + at(i0 + i) * D + lane * E;
-      float v[E];
-      if (E == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        v[0] = f.x;
-        v[1] = f.y;
-        v[2 % E] = f.z;
-        v[3 % E] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        v[0] = f.x;
-        v[1] = f.y;
-      }
-      if (wi != 0.f)
+    for (int i = 0; i < cnt; i += kAhead) {
+      if (i != 0) load(i0 + i, cnt - i);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wi * v[e];
+      for (int y = 0; y < kAhead; ++y) {
+        const float wi = __shfl_sync(0xffffffffu, w, (i + y) & 31);
+        if (i + y < cnt && wi != 0.f)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += wi * v[y][e];
+      }
     }
   }
   const int h = kh * p.g + r / p.Nq, i = r % p.Nq;
