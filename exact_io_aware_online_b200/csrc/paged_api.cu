@@ -181,9 +181,9 @@ EncodeTiledFn encode_tiled() {
 }
 
 // Pages [num_pages, Hkv, page_size, d] in boxes of `box` tokens of one page and
-// head: rows of 128 bytes (64 where a row has no more) with the swizzle of that
+// `heads` heads: rows of 128 bytes (64 where a row has no more) with the swizzle of that
 // width.  Tokens behind the page's end and a page number of num_pages read as zero.
-bool page_map(CUtensorMap* m, const void* base, const fa::CacheParams& c, int d, bool quant, int box) {
+bool page_map(CUtensorMap* m, const void* base, const fa::CacheParams& c, int d, bool quant, int box, int heads) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const int es = quant ? 1 : 2;
@@ -192,7 +192,8 @@ bool page_map(CUtensorMap* m, const void* base, const fa::CacheParams& c, int d,
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.pages.n) * es, static_cast<cuuint64_t>(c.pages.h) * es,
                                  static_cast<cuuint64_t>(c.pages.b) * es};
   const int inner = std::min(d * es, 128);
-  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(inner / es), static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(inner / es), static_cast<cuuint32_t>(box),
+                               static_cast<cuuint32_t>(heads), 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
   return enc(m, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
              dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -212,12 +213,14 @@ PagedOffsets paged_offsets(int rows, int d) {
   return w;
 }
 
-int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // rows of a unit
+int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // rows of a kv head in a unit
+// kv heads of a unit: as many as leave each warp rows of its own, where they divide Hkv
+int paged_heads(int R, int Hkv) { return R <= 8 && Hkv % 4 == 0 ? 4 : R > 8 && R <= 16 && Hkv % 2 == 0 ? 2 : 1; }
 
-template <int D, bool kQuant, int NB, int RG>
-fa_status launch_paged(fa::PagedParams p, const CUtensorMap* maps, double tiles, cudaStream_t st) {
-  using C = fa::PagedCfg<D, kQuant, NB, RG>;
-  const auto kernel = fa::paged_kernel<D, kQuant, NB, RG>;
+template <int D, bool kQuant, int NB, int RG, int HG>
+fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStream_t st) {
+  using C = fa::PagedCfg<D, kQuant, NB, RG, HG>;
+  const auto kernel = fa::paged_kernel<D, kQuant, NB, RG, HG>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   static std::atomic<uint64_t> ready{0};  // devices on which this kernel may use its shared memory
@@ -227,25 +230,38 @@ fa_status launch_paged(fa::PagedParams p, const CUtensorMap* maps, double tiles,
       return FA_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_release);
   }
+  p.box_log = 3;
+  while (p.box_log < 5 && p.pad_page % (2 << p.box_log) == 0 && C::kTile % (2 << p.box_log) == 0) ++p.box_log;
+  CUtensorMap mk, mv;
+  if (!page_map(&mk, cache->k_pages, p.c, D, kQuant, 1 << p.box_log, HG) ||
+      !page_map(&mv, cache->v_pages, p.c, D, kQuant, 1 << p.box_log, HG))
+    return FA_ERR_CUDA;
   // lanes: the largest divisor of a sequence's units that leaves at most one CTA in sixteen without work
-  const int units = p.c.Hkv * p.nblk, most = 148 * C::kCtas;
+  const int units = p.c.Hkv / HG * p.nblk, most = 148 * C::kCtas;
   p.lanes = std::min(units, most);
   while (units % p.lanes != 0 || most % p.lanes > most / 16) --p.lanes;
   // no more groups than the lengths could give tiles
-  const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles));
-  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, maps[0], maps[1], p);
+  const long long cap = static_cast<long long>(p.c.max_pages) * p.pad_page;
+  const double tiles = static_cast<double>((cap + C::kTile - 1) / C::kTile) * p.c.B;  // of one unit of each sequence
+  // tiles are counted in 32 bits: those of a CTA, and of all sequences
+  if (tiles > 2e9 || tiles * units / most > 1e9) return FA_ERR_UNSUPPORTED;
+  const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles * (units / p.lanes)));
+  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, mk, mv, p);
   if (s != FA_OK) return s;
-  const dim3 grid(ctas, (p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
-  return launch(fa::paged_combine_kernel<D, kQuant>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, C::kRows);
+  const dim3 grid(ctas, (HG * p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
+  return launch(fa::paged_combine_kernel<D, kQuant>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, C::kRows, HG);
 }
 
 template <int D, bool kQuant>
-fa_status launch_paged_rows(const fa::PagedParams& p, const CUtensorMap* maps, double tiles, cudaStream_t st) {
+fa_status launch_paged_rows(const fa_paged_cache* cache, const fa::PagedParams& p, cudaStream_t st) {
+  const int heads = paged_heads(p.R, p.c.Hkv);
   switch (paged_rows(p.R)) {
-    case 8: return launch_paged<D, kQuant, 1, 1>(p, maps, tiles, st);
-    case 16: return launch_paged<D, kQuant, 1, 2>(p, maps, tiles, st);
-    case 32: return launch_paged<D, kQuant, 1, 4>(p, maps, tiles, st);
-    default: return launch_paged<D, kQuant, 2, 4>(p, maps, tiles, st);
+    case 8:
+      return heads == 4 ? launch_paged<D, kQuant, 1, 1, 4>(cache, p, st) : launch_paged<D, kQuant, 1, 1, 1>(cache, p, st);
+    case 16:
+      return heads == 2 ? launch_paged<D, kQuant, 1, 2, 2>(cache, p, st) : launch_paged<D, kQuant, 1, 2, 1>(cache, p, st);
+    case 32: return launch_paged<D, kQuant, 1, 4, 1>(cache, p, st);
+    default: return launch_paged<D, kQuant, 2, 4, 1>(cache, p, st);
   }
 }
 
@@ -286,7 +302,8 @@ fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_
 size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d) {
   if (!paged_sizes_ok(B, H, Hkv, Nq) || (d != 64 && d != 128)) return 0;
   const long long R = static_cast<long long>(H / Hkv) * Nq;
-  return paged_offsets(static_cast<int>(std::min(R, 64LL)), d).bytes;
+  const int r = static_cast<int>(std::min(R, 64LL));
+  return paged_offsets(paged_heads(r, Hkv) * r, d).bytes;
 }
 
 fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,
@@ -321,25 +338,16 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.nblk = (p.R + block - 1) / block;
   p.prow = std::min(p.R, block);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const PagedOffsets at = paged_offsets(p.prow, d);
+  const PagedOffsets at = paged_offsets(paged_heads(p.R, Hkv) * p.prow, d);
   p.split = reinterpret_cast<int4*>(ws);
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
   p.pad_page = (cache->page_size + 7) & ~7;
-  p.box_log = p.pad_page % 32 == 0 ? 5 : p.pad_page % 16 == 0 ? 4 : 3;
   magic(p.pad_page, &p.pad_mul, &p.pad_shift);
-  const long long cap = static_cast<long long>(cache->max_pages) * p.pad_page;
-  if (cap > (1LL << 30)) return FA_ERR_UNSUPPORTED;  // padded positions are 32-bit too
-  const double tiles = static_cast<double>((cap + 63) / 64) * B * Hkv * p.nblk;  // at most
-  // tiles are counted in 32 bits: a CTA's, and all sequences' of one head
-  if (tiles / 148 > 1e9 || static_cast<double>((cap + 63) / 64) * B > 2e9) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(cache->max_pages) * p.pad_page > (1LL << 30)) return FA_ERR_UNSUPPORTED;  // padded positions are 32-bit too
   const bool quant = cache->dtype == FA_CACHE_E4M3;
-  CUtensorMap maps[2];
-  if (!page_map(&maps[0], cache->k_pages, p.c, d, quant, 1 << p.box_log) ||
-      !page_map(&maps[1], cache->v_pages, p.c, d, quant, 1 << p.box_log))
-    return FA_ERR_CUDA;
-  if (d == 64) return quant ? launch_paged_rows<64, true>(p, maps, tiles, st) : launch_paged_rows<64, false>(p, maps, tiles, st);
-  return quant ? launch_paged_rows<128, true>(p, maps, tiles, st) : launch_paged_rows<128, false>(p, maps, tiles, st);
+  if (d == 64) return quant ? launch_paged_rows<64, true>(cache, p, st) : launch_paged_rows<64, false>(cache, p, st);
+  return quant ? launch_paged_rows<128, true>(cache, p, st) : launch_paged_rows<128, false>(cache, p, st);
 }
 
 }  // extern "C"

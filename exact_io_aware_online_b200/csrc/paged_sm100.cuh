@@ -14,8 +14,8 @@
 // transposed, S^T = K Q^T and O^T = V^T P^T, so that the 16 of m16n8k16 is
 // filled by keys and by columns of V and only the rows are padded, to 8.
 //
-// Work: the keys that some row of a unit (sequence, kv head, block of rows) may
-// see are cut into tiles of 64 or 128.  The CTAs form groups of `lanes`, a lane
+// Work: the keys that some row of a unit (sequence, 1 to 4 kv heads, block of
+// rows) may see are cut into tiles of 16 to 128, about 32 KB.  The CTAs form groups of `lanes`, a lane
 // for each unit of a sequence (or every lanes-th), so that a group reads the
 // same tokens' heads at the same time: heads inside tokens are then whole DRAM
 // rows, the 32-byte sectors of the scales are read from DRAM once, and blocks
@@ -23,8 +23,11 @@
 // group c of G takes its c-th even share, whatever the lengths (beginning a
 // unit counts as much as a tile).  In each CTA one warp walks the share, looks
 // pages up and keeps a ring of tiles loading (TMA boxes of 8 to 32 tokens, each
-// inside a page; scales by cp.async), on from one unit into the next; four
-// warps compute.  A unit that lies in one share is finished by its CTA; one that several share leaves a partial (m, l,
+// inside a page, over the unit's kv heads; scales by cp.async), on from one unit
+// into the next; four warps compute, where the kv heads allow it each its own
+// head or rows, so that they never meet; otherwise they share a tile's keys and
+// join their states at a unit's end.  A unit that lies in one share is finished
+// by its CTA; one that several share leaves a partial (m, l,
 // accumulator) per CTA -- at most two per CTA, so the workspace does not grow
 // with the batch -- for paged_combine_kernel.
 //
@@ -54,35 +57,40 @@ struct PagedParams {
   int H, Nq, g;  // g = H / Hkv
   float scale_log2;
   int causal, window;
-  int R, nblk;     // rows of a kv head (g * Nq), units they make
-  int lanes;       // CTAs of a group: a divisor of Hkv * nblk
+  int R, nblk;     // rows of a kv head (g * Nq), blocks they make
+  int lanes;       // CTAs of a group: a divisor of a sequence's units
   int pad_page;    // page_size rounded up to a multiple of 8
   uint32_t pad_mul;  // pos / pad_page, as CacheParams::page_mul
   int pad_shift;
   int box_log;     // log2 of the tokens of a TMA box: 3 to 5
   int prow;        // rows of a partial: min(R, rows of a unit)
-  float* part_o;   // [2 * G][prow][D]
-  float4* part_m;  // [2 * G][prow]: m, l, unit of the accumulator
+  float* part_o;   // [2 * G][kv heads of a unit][prow][D]
+  float4* part_m;  // [2 * G][kv heads of a unit][prow]: m, l, unit of the accumulator
   int4* split;     // [CTAs]: the unit that starts in CTA c and goes on in its lane: b, unit, CTAs it spans (or 0)
 };
 
-// A warp holds NB blocks of 8 rows; RG groups of warps hold different rows, the
-// kPagedWarps / RG warps of a group share each tile's keys.
-template <int D, bool kQuant, int NB, int RG>
+// A unit has HG kv heads and up to 8 * NB * RG rows of each: a warp holds NB
+// blocks of 8 rows of one head, and KW = 4 / (HG * RG) warps share each tile's
+// keys.
+template <int D, bool kQuant, int NB, int RG, int HG>
 struct PagedCfg {
-  static constexpr int kRows = 8 * NB * RG;  // rows of a unit
+  static constexpr int kRows = 8 * NB * RG;
+  static constexpr int KW = kPagedWarps / (HG * RG);
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
-  static constexpr int kTile = kRowBytes == 256 ? 64 : 128;  // keys
+  static constexpr int kTile = (kRowBytes == 256 || (kQuant && KW == 4 && D == 128) ? 64 : 128) / HG;  // keys
   static constexpr int kPart = kRowBytes == 256 ? 128 : kRowBytes;  // bytes of a row in a TMA box (its swizzle's width)
-  static constexpr int kTileBytes = kTile * kRowBytes;
+  static constexpr int kTileBytes = HG * kTile * kRowBytes;
+  static constexpr int kScaleBytes = kQuant ? HG * kTile * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + (kQuant ? 1024 : 0);  // K, V, scales of K and of V
   static constexpr int kCtas = D == 128 && NB == 2 ? 2 : 3;  // of an SM
   static constexpr int kStages = (226 * 1024 / kCtas - 2048) / kStageBytes < 4 ? (226 * 1024 / kCtas - 2048) / kStageBytes : 4;
   static constexpr int kMergeStride = D + 4;  // floats; 2 * stride = 8 mod 32: a warp's stores meet every bank once
-  static constexpr int kStatBytes = kPagedWarps * 8 * NB * 16;
+  static constexpr int kStatBytes = KW > 1 ? kPagedWarps * 8 * NB * 16 : 0;
   static constexpr int kSmemBytes = kStages * (kStageBytes + 16 + 48) + kStatBytes + 16 + 128;
   static_assert(kStages >= 2, "a tile loads while another is computed");
-  static_assert(kPagedWarps * 8 * kMergeStride * 4 <= kStageBytes, "the warps' accumulators are joined in a stage");
+  static_assert(2 * kScaleBytes <= 1024, "both tiles' scales fit behind the values");
+  static_assert(KW == 1 || (HG == 1 && kPagedWarps * 8 * kMergeStride * 4 <= kStageBytes),
+                "the warps' accumulators are joined in a stage");
 };
 
 // 4 bytes to shared memory, zero when !on.
@@ -162,25 +170,28 @@ __device__ __forceinline__ int paged_tiles(const PagedParams& p, int L) {
   return (s.y - s.x + kTile - 1) / kTile;
 }
 
+__device__ __forceinline__ int pad_page_of(const PagedParams& p, int padded) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(padded)) * p.pad_mul) >> (31 + p.pad_shift));
+}
 __device__ __forceinline__ int paged_slot(const PagedParams& p, int padded) {  // the token inside its page
-  return padded - static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(padded)) * p.pad_mul) >>
-                                   (31 + p.pad_shift)) * p.pad_page;
+  return padded - pad_page_of(p, padded) * p.pad_page;
 }
 
 struct PagedDesc {  // a tile, as the loading warp describes it to the others
-  int b, unit, key0, end, flags, L;
+  int b, unit, key0, end;
+  int flags, L;
   uint32_t boxes;         // those that are on a page
   int next_b, next_unit;  // of the tile after it
   int pad[3];
 };
 constexpr int kFlagUnitStart = 1, kFlagUnitEnd = 2, kFlagSegEnd = 4;
 
-template <int D, bool kQuant, int NB, int RG>
-__global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kCtas)
+template <int D, bool kQuant, int NB, int RG, int HG>
+__global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>::kCtas)
     paged_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ PagedParams p) {
-  using C = PagedCfg<D, kQuant, NB, RG>;
-  constexpr int KW = kPagedWarps / RG;        // warps that share a tile's keys
+  using C = PagedCfg<D, kQuant, NB, RG, HG>;
+  constexpr int KW = C::KW;                   // warps that share a tile's keys
   constexpr int DT = D / 16;                  // row tiles of O^T = V^T P^T
   constexpr int QS = D / 16;                  // k-steps of S^T = K Q^T
   constexpr int ST = C::kStages, RB = C::kRowBytes, PB = C::kPart, TK = C::kTile;
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   constexpr int ES = kQuant ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   float4* stat = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);     // [warps][8 * NB rows]: m, l, unit
-  PagedDesc* desc = reinterpret_cast<PagedDesc*>(stat + kPagedWarps * 8 * NB);  // [ST]
+  PagedDesc* desc = reinterpret_cast<PagedDesc*>(smem + ST * C::kStageBytes + C::kStatBytes);  // [ST]
   uint64_t* full = reinterpret_cast<uint64_t*>(desc + ST);                  // [ST]
   uint64_t* empty = full + ST;                                              // [ST]
   uint64_t* joined = empty + ST;
@@ -198,7 +209,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, B = p.c.B;
   const int group = cta / p.lanes, ulane = cta - group * p.lanes, groups = gridDim.x / p.lanes;
-  const int U = p.c.Hkv * p.nblk / p.lanes;  // units of a sequence in a lane: ulane + lanes * (0 .. U - 1)
+  const int U = p.c.Hkv / HG * p.nblk / p.lanes;  // units of a sequence in a lane: ulane + lanes * (0 .. U - 1)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(full + i, kQuant ? 33 : 1);
@@ -303,6 +314,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       int b, u, key0, end, flags, L;
       int page, slot;  // of box `lane`
     };
+    // the page table's entries for the sequence after this one on their way into L2
+    auto prefetch = [&] {
+      if (fLnext == 0 || lane >= TK >> p.box_log) return;
+      const int2 s = paged_span(p, fLnext);
+      const int pos = s.x + (lane << p.box_log);
+      if (pos < s.y)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.c.table + (fb + 1) * p.c.table_stride + pad_page_of(p, pos)));
+    };
     // the n-th tile; moves the cursor on
     auto fetch = [&](int n) {
       Tile t = {0, 0, 0, 0, 0, 0, -1, 0};
@@ -316,8 +335,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
                 (n == cnt - 1 ? kFlagSegEnd : 0);
       const int pos = t.key0 + (lane << p.box_log);
       if (lane < TK >> p.box_log && pos < t.end) {
-        const int i = static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(pos)) * p.pad_mul) >>
-                                       (31 + p.pad_shift));
+        const int i = pad_page_of(p, pos);
         t.slot = pos - i * p.pad_page;
         t.page = p.c.table[fb * p.c.table_stride + i];
       }
@@ -333,11 +351,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
               fnt = paged_tiles<TK>(p, fL);
             } while (fnt == 0 && fb < B - 1);
             span = paged_span(p, fL);
+            prefetch();
           }
         }
       }
       return t;
     };
+    prefetch();
     Tile cur = fetch(0);
     int st = 0, ph = 1;
     int n = 0;
@@ -348,20 +368,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       const uint32_t boxes = __ballot_sync(0xffffffffu, on);
       // boxes up to the end of the last group of 32 keys; those on no page are filled with zeros
       const int live = min(TK, (cur.end - cur.key0 + 31) & ~31) >> p.box_log;
-      const int kh = p.nblk == 1 ? cur.u : cur.u / p.nblk;
+      const int kh = (p.nblk == 1 ? cur.u : cur.u / p.nblk) * HG;
       uint8_t* dst = smem + st * C::kStageBytes;
       if (lane == 0) {
-        PagedDesc& t = desc[st];
-        t.b = cur.b;
-        t.unit = cur.u;
-        t.key0 = cur.key0;
-        t.end = cur.end;
-        t.flags = cur.flags;
-        t.L = cur.L;
-        t.boxes = boxes;
-        t.next_b = next.b;
-        t.next_unit = next.u;
-        mbar_arrive_expect_tx(full + st, (live << p.box_log) * 2 * RB);
+        int4* t = reinterpret_cast<int4*>(desc + st);
+        t[0] = make_int4(cur.b, cur.u, cur.key0, cur.end);
+        t[1] = make_int4(cur.flags, cur.L, static_cast<int>(boxes), next.b);
+        t[2] = make_int4(next.u, 0, 0, 0);
+        mbar_arrive_expect_tx(full + st, (live << p.box_log) * 2 * RB * HG);
       }
       const int page = on ? cur.page : p.c.num_pages;
       for (int i0 = 0; i0 < live; i0 += 4) {
@@ -375,21 +389,22 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (i0 + i >= live) break;
-          uint8_t* to = dst + ((i0 + i) << p.box_log) * PB;
+          uint8_t* to = dst + ((i0 + i) << p.box_log) * HG * PB;
 #pragma unroll
           for (int h = 0; h < RB / PB; ++h) {
-            tma_load_4d(&map_k, full + st, to + h * TK * PB, h * PB / ES, slot[i], kh, pg[i]);
-            tma_load_4d(&map_v, full + st, to + h * TK * PB + C::kTileBytes, h * PB / ES, slot[i], kh, pg[i]);
+            tma_load_4d(&map_k, full + st, to + h * HG * TK * PB, h * PB / ES, slot[i], kh, pg[i]);
+            tma_load_4d(&map_v, full + st, to + h * HG * TK * PB + C::kTileBytes, h * PB / ES, slot[i], kh, pg[i]);
           }
         }
       }
       if (kQuant) {
         const long long at = on ? p.c.scales.row(cur.page, kh, cur.slot) : -1;
-        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes) + lane * 4;
-        long long off[TK / 32];
-        bool here[TK / 32];
+        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes) + lane * 4;  // [heads][keys]
+        constexpr int TL = TK < 32 ? 32 : TK;  // a head's entries, in groups of 32
+        long long off[TL / 32];
+        bool here[TL / 32];
 #pragma unroll
-        for (int i = 0; i < TK / 32; ++i) {
+        for (int i = 0; i < TL / 32; ++i) {
           const int src = (i * 32 + lane) >> p.box_log, in = lane & (box - 1);
           off[i] = __shfl_sync(0xffffffffu, at, src);
           const int slot = __shfl_sync(0xffffffffu, cur.slot, src) + in;
@@ -397,10 +412,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
           off[i] += in * p.c.scales.n;
         }
 #pragma unroll
-        for (int i = 0; i < TK / 32; ++i) {
-          cp_async4(to + i * 128, p.c.ks + (here[i] ? off[i] : 0), here[i]);
-          cp_async4(to + i * 128 + 512, p.c.vs + (here[i] ? off[i] : 0), here[i]);
-        }
+        for (int h = 0; h < HG; ++h)
+#pragma unroll
+          for (int i = 0; i < TL / 32; ++i) {
+            if (TK < 32 && lane >= TK) break;
+            const long long from = here[i] ? off[i] + h * p.c.scales.h : 0;
+            cp_async4(to + (h * TK + i * 32) * 4, p.c.ks + from, here[i]);
+            cp_async4(to + (h * TK + i * 32) * 4 + C::kScaleBytes, p.c.vs + from, here[i]);
+          }
         cp_async_arrive(full + st);
       }
       cur = next;
@@ -413,7 +432,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   }
 
   // ---- a computing warp's rows and its share of a tile's keys
-  const int rg = warp / KW, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
+  const int hg = warp / (RG * KW), rg = warp / KW % RG, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
   uint32_t qb[NB][QS][2];  // Q^T: row rq of each block, the k index in the order of the K fragments
   float acc[NB][DT][4];    // O^T: columns dcol(x, 0), dcol(x, 1) of V for rows 2 qd, 2 qd + 1
   float m[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2];
@@ -424,7 +443,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
   // the queries of a unit, as they are in memory: words (8 s + qd, + 4) of a row, or its words 8 s + 2 qd, + 1 where
   // the K fragments are taken from 16 codes at a time
   auto load_q = [&](int b, int unit) {
-    const int kh = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - kh * p.nblk) * C::kRows + rg * 8 * NB;
+    const int ku = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - ku * p.nblk) * C::kRows + rg * 8 * NB;
+    const int kh = ku * HG + hg;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = row0 + nb * 8 + rq;
@@ -455,15 +475,20 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
     if (lane == 0) mbar_arrive(empty + st);
     if (++st == ST) st = 0, ph ^= 1;
   };
-  // a lane's row in a fragment of 16 keys x 32 bytes; parts of a row are kTile * kPart apart, their 16-byte units
-  // swizzled by the TMA: unit ^ (key & 7) (128 bytes), unit ^ (key / 2 & 3) (64 bytes)
+  // A stage holds [part of a row][box][head][token of the box][part bytes], the
+  // 16-byte units swizzled by the TMA: unit ^ (token & 7) (parts of 128 bytes),
+  // unit ^ (token / 2 & 3) (64).  Keys 16 i + (0 .. 15) are in one box or two.
   auto swz = [](int key) { return PB == 128 ? key & 7 : (key >> 1) & 3; };
-  auto part = [](int i) { return i * 32 / PB * TK * PB; };
-  const int kkey = (lane & 7) + ((lane >> 3) & 1) * 8, vkey = (lane & 7) + ((lane >> 4) << 3);
-  const uint32_t kat = kkey * PB + (((lane >> 4) ^ swz(kkey)) << 4);
-  const uint32_t vat = vkey * PB + ((((lane >> 3) & 1) ^ swz(vkey)) << 4);
-  auto v_at = [&](int key, int byte) {  // of a row of V
-    return byte / PB * TK * PB + key * PB + ((((byte % PB) >> 4) ^ swz(key)) << 4) + (byte & 15);
+  auto part = [](int i) { return i * 32 / PB * HG * TK * PB; };
+  const int half = p.box_log == 3 ? HG * 8 * PB : 8 * PB;  // from key 16 i to 16 i + 8
+  auto group_at = [&](int key) {  // key = 16 i, of this warp's head
+    return (((key >> p.box_log) * HG + hg) << p.box_log) * PB + (key & ((1 << p.box_log) - 1)) * PB;
+  };
+  // a lane's row in a fragment of 16 keys x 32 bytes of K, of V (transposed)
+  const uint32_t kat = (lane & 7) * PB + ((lane >> 3) & 1) * half + (((lane >> 4) ^ swz(lane & 7)) << 4);
+  const uint32_t vat = (lane & 7) * PB + (lane >> 4) * half + ((((lane >> 3) & 1) ^ swz(lane & 7)) << 4);
+  auto v_at = [&](int key, int byte) {  // of row key = 0 .. 15 of a group of V
+    return byte / PB * HG * TK * PB + (key & 7) * PB + (key >> 3) * half + ((((byte % PB) >> 4) ^ swz(key)) << 4) + (byte & 15);
   };
 
   load_q(fb, fu * p.lanes + ulane);
@@ -526,260 +551,260 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
 
     const uint8_t* pV = smem + st * C::kStageBytes + C::kTileBytes;
     const uint32_t kaddr = smem_u32(smem + st * C::kStageBytes) + kat, vaddr = smem_u32(pV) + vat;
-    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes);  // K's, 128 further V's
+    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes) + hg * TK;  // K's, HG * TK further V's
     // the steps of a tile; kEdge: some row may not see some key of it
     auto steps = [&](auto edge_tile) {
       constexpr bool edge = decltype(edge_tile)::value;
 #pragma unroll 1
-    for (int s = 0; s < TK / KW / (16 * KS); ++s) {
-      const int kb = (kw * (TK / KW / (16 * KS)) + s) * 16 * KS;
-      if (edge && kb >= left) break;  // behind the end
-      // ---- S^T of keys 16 k + rq (elements 0, 1) and 16 k + rq + 8 (2, 3), rows 2 qd and 2 qd + 1
-      float sc[KS][NB][4];
+      for (int s = 0; s < TK / KW / (16 * KS); ++s) {
+        const int kb = (kw * (TK / KW / (16 * KS)) + s) * 16 * KS;
+        if (edge && kb >= left) break;  // behind the end
+        // ---- S^T of keys 16 k + rq (elements 0, 1) and 16 k + rq + 8 (2, 3), rows 2 qd and 2 qd + 1
+        float sc[KS][NB][4];
+        int at[KS];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
+        for (int k = 0; k < KS; ++k) {
+          at[k] = group_at(kb + 16 * k);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[k][nb][0] = sc[k][nb][1] = sc[k][nb][2] = sc[k][nb][3] = 0.f;
-        constexpr int NL = RB / 32;  // 32 bytes of 16 keys a load
-        uint32_t a[NL][4];
+          for (int nb = 0; nb < NB; ++nb) sc[k][nb][0] = sc[k][nb][1] = sc[k][nb][2] = sc[k][nb][3] = 0.f;
+          constexpr int NL = RB / 32;  // 32 bytes of 16 keys a load
+          uint32_t a[NL][4];
 #pragma unroll
-        for (int i = 0; i < NL; ++i) ldmatrix_x4(a[i], (kaddr + part(i) + (kb + 16 * k) * PB) ^ ((i << 5) & (PB - 1)));
+          for (int i = 0; i < NL; ++i) ldmatrix_x4(a[i], (kaddr + at[k] + part(i)) ^ ((i << 5) & (PB - 1)));
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          if (kQuant) {
+          for (int i = 0; i < NL; ++i) {
+            if (kQuant) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(a[i][2 * y], &a0, &a2);
-              e4m3x4_to_f16(a[i][2 * y + 1], &a1, &a3);
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(a[i][2 * y], &a0, &a2);
+                e4m3x4_to_f16(a[i][2 * y + 1], &a1, &a3);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[k][nb], a0, a1, a2, a3, qb[nb][(2 * i + y) % QS]);
+                for (int nb = 0; nb < NB; ++nb) mma16<true>(sc[k][nb], a0, a1, a2, a3, qb[nb][(2 * i + y) % QS]);
+              }
+            } else {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<false>(sc[k][nb], a[i][0], a[i][1], a[i][2], a[i][3], qb[nb][i % QS]);
             }
-          } else {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16<false>(sc[k][nb], a[i][0], a[i][1], a[i][2], a[i][3], qb[nb][i % QS]);
           }
         }
-      }
-      float vs[KS][2];
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ks = kQuant ? scl[kb + 16 * k + 8 * h + rq] : 1.f;
-          vs[k][h] = kQuant ? scl[128 + kb + 16 * k + 8 * h + rq] : 1.f;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              sc[k][nb][2 * h + c] *= rowf[nb][c];
-              if (kQuant) sc[k][nb][2 * h + c] *= ks;
-            }
-        }
-      uint32_t allowed = 0xffffffffu;  // bit 4 (k NB + nb) + e
-      if (edge) {
-        allowed = 0;
-        const int j0 = key0 + kb + rq;
-        bool here[KS][2];  // key 16 k + 8 h + rq exists (8 keys in line are in one box)
+        float vs[KS][2];
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            here[k][h] = (boxes >> ((kb + 16 * k + 8 * h) >> p.box_log)) & 1;
-            if (p.pad_page != p.c.page_size) here[k][h] &= paged_slot(p, j0 + 16 * k + 8 * h) < p.c.page_size;
+            const float ks = kQuant ? scl[kb + 16 * k + 8 * h + rq] : 1.f;
+            vs[k][h] = kQuant ? scl[HG * TK + kb + 16 * k + 8 * h + rq] : 1.f;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                sc[k][nb][2 * h + c] *= rowf[nb][c];
+                if (kQuant) sc[k][nb][2 * h + c] *= ks;
+              }
           }
+        uint32_t allowed = 0xffffffffu;  // bit 4 (k NB + nb) + e
+        if (edge) {
+          allowed = 0;
+          const int j0 = key0 + kb + rq;
+          bool here[KS][2];  // key 16 k + 8 h + rq exists (8 keys in line are in one box)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+          for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int lo = rlo[nb][c] - j0, hi = rhi[nb][c] - j0;
+            for (int h = 0; h < 2; ++h) {
+              here[k][h] = (boxes >> ((kb + 16 * k + 8 * h) >> p.box_log)) & 1;
+              if (p.pad_page != p.c.page_size) here[k][h] &= paged_slot(p, j0 + 16 * k + 8 * h) < p.c.page_size;
+            }
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (here[k][h] && 16 * k + 8 * h >= lo && 16 * k + 8 * h < hi)
-                  allowed |= 1u << (4 * (k * NB + nb) + 2 * h + c);
-                else
-                  sc[k][nb][2 * h + c] = -INFINITY;
-          }
-      }
-      auto on = [&](int k, int nb, int e) { return !edge || ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
-      // ---- running maximum: moved only when it grows by more than 8 (weights
-      // stay below 2^8).  Quantised: weights reach the second product as f16
-      // multiples of the largest value scale so far (vref, a power of two above
-      // it); a row's accumulator counts in units of its vref.
-      bool grow = false;
-      float mx[NB][2];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mx[nb][c] = fmaxf(sc[0][nb][c], sc[0][nb][2 + c]);
-          if (KS == 2) mx[nb][c] = fmaxf(mx[nb][c], fmaxf(sc[KS - 1][nb][c], sc[KS - 1][nb][2 + c]));
-          grow |= mx[nb][c] > m[nb][c] + 8.f;
-          if (kQuant)
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) grow |= fabsf(vs[k][h]) >= vref[nb][c] && on(k, nb, 2 * h + c);
-        }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t ve = 0;
-            if (kQuant)
+            for (int c = 0; c < 2; ++c) {
+              const int lo = rlo[nb][c] - j0, hi = rhi[nb][c] - j0;
 #pragma unroll
               for (int k = 0; k < KS; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                  if (on(k, nb, 2 * h + c)) ve = max(ve, (__float_as_uint(vs[k][h]) >> 23) & 0xffu);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-              mx[nb][c] = fmaxf(mx[nb][c], __shfl_xor_sync(0xffffffffu, mx[nb][c], o));
-              if (kQuant) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, o));
+                  if (here[k][h] && 16 * k + 8 * h >= lo && 16 * k + 8 * h < hi)
+                    allowed |= 1u << (4 * (k * NB + nb) + 2 * h + c);
+                  else
+                    sc[k][nb][2 * h + c] = -INFINITY;
             }
-            const float mn = mx[nb][c] > m[nb][c] + 8.f ? mx[nb][c] : m[nb][c];
-            float f = m[nb][c] == mn ? 1.f : exp2_fast(m[nb][c] - mn);
-            m[nb][c] = mn;
-            l[nb][c] *= f;
-            if (kQuant) {
-              const float vn = fmaxf(vref[nb][c], __uint_as_float(min(ve + 1u, 253u) << 23));
-              vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
-              f *= vref[nb][c] * vinv[nb][c];
-              vref[nb][c] = vn;
-            }
-#pragma unroll
-            for (int x = 0; x < DT; ++x) {
-              acc[nb][x][c] *= f;
-              acc[nb][x][2 + c] *= f;
-            }
-          }
-      }
-      // The weights are rounded to 16 bits for the second product: bf16 (half a
-      // step is 2^-8 of a weight), or f16 of weight * value scale / vref, 2^-11
-      // of it down to 2^-14; keys whose scale is below 2^-12 vref take the slow
-      // form below.
-      uint32_t pb[KS][NB][2];
-      bool slow[KS];
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        slow[k] = false;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float mu = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
-            const float w = exp2_fast(sc[k][nb][e] - mu);
-            l[nb][e & 1] += w;
-            sc[k][nb][e] = w;
-            if (kQuant) {
-              const float u = vs[k][e >> 1] * vinv[nb][e & 1];
-              slow[k] |= on(k, nb, e) && fabsf(u) < 0x1p-12f && fabsf(vs[k][e >> 1]) > 0x1p-90f;
-              sc[k][nb][e] = on(k, nb, e) ? w * u : 0.f;
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            pb[k][nb][h] = transpose8x8(kQuant ? pack_f16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1])
-                                               : pack_bf16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1]));
         }
-      }
-      // The slow form of columns dcol(x0 .. x0 + 3, .): products one by one in
-      // fp32, weights of zero left out.  For an infinity or NaN among the values
-      // of a tile that some rows see only in part (0 * infinity would reach rows
-      // that may not see that key), and for value scales too far apart for f16.
-      auto one_by_one = [&](int k, int x0) {
-#pragma unroll 1
-        for (int y = 0; y < 16; ++y)
+        auto on = [&](int k, int nb, int e) { return !edge || ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
+        // ---- running maximum: moved only when it grows by more than 8 (weights
+        // stay below 2^8).  Quantised: weights reach the second product as f16
+        // multiples of the largest value scale so far (vref, a power of two above
+        // it); a row's accumulator counts in units of its vref.
+        bool grow = false;
+        float mx[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mx[nb][c] = fmaxf(sc[0][nb][c], sc[0][nb][2 + c]);
+            if (KS == 2) mx[nb][c] = fmaxf(mx[nb][c], fmaxf(sc[KS - 1][nb][c], sc[KS - 1][nb][2 + c]));
+            grow |= mx[nb][c] > m[nb][c] + 8.f;
+            if (kQuant)
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) grow |= fabsf(vs[k][h]) >= vref[nb][c] && on(k, nb, 2 * h + c);
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t ve = 0;
+              if (kQuant)
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if (on(k, nb, 2 * h + c)) ve = max(ve, (__float_as_uint(vs[k][h]) >> 23) & 0xffu);
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) {
+                mx[nb][c] = fmaxf(mx[nb][c], __shfl_xor_sync(0xffffffffu, mx[nb][c], o));
+                if (kQuant) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, o));
+              }
+              const float mn = mx[nb][c] > m[nb][c] + 8.f ? mx[nb][c] : m[nb][c];
+              float f = m[nb][c] == mn ? 1.f : exp2_fast(m[nb][c] - mn);
+              m[nb][c] = mn;
+              l[nb][c] *= f;
+              if (kQuant) {
+                const float vn = fmaxf(vref[nb][c], __uint_as_float(min(ve + 1u, 253u) << 23));
+                vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
+                f *= vref[nb][c] * vinv[nb][c];
+                vref[nb][c] = vn;
+              }
+#pragma unroll
+              for (int x = 0; x < DT; ++x) {
+                acc[nb][x][c] *= f;
+                acc[nb][x][2 + c] *= f;
+              }
+            }
+        }
+        // The weights are rounded to 16 bits for the second product: bf16 (half a
+        // step is 2^-8 of a weight), or f16 of weight * value scale / vref, 2^-11
+        // of it down to 2^-14; keys whose scale is below 2^-12 vref take the slow
+        // form below.
+        uint32_t pb[KS][NB][2];
+        bool slow[KS];
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          slow[k] = false;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const int src = (y & 7) * 4 + qd;
-            const float f0 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][0] : sc[k][nb][2], src);
-            const float f1 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][1] : sc[k][nb][3], src);
 #pragma unroll
-            for (int x = x0; x < x0 + 4; ++x)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint8_t* at = pV + v_at(kb + 16 * k + y, dcol(x, e) * ES);
-                const float v = kQuant ? e4m3x2_to_float2(*at).x
-                                       : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) << 16);
-                if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
-                if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
+            for (int e = 0; e < 4; ++e) {
+              const float mu = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
+              const float w = exp2_fast(sc[k][nb][e] - mu);
+              l[nb][e & 1] += w;
+              sc[k][nb][e] = w;
+              if (kQuant) {
+                const float u = vs[k][e >> 1] * vinv[nb][e & 1];
+                slow[k] |= on(k, nb, e) && fabsf(u) < 0x1p-12f && fabsf(vs[k][e >> 1]) > 0x1p-90f;
+                sc[k][nb][e] = on(k, nb, e) ? w * u : 0.f;
               }
-          }
-      };
-      // ---- O^T += V^T P^T
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int kk = kb + 16 * k;
-        if (kQuant) {
-          uint32_t w[4][D / 32];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint8_t* v = pV + v_at(kk + 2 * qd + (y & 1) + 8 * (y >> 1), rq * (D / 8));
-            if (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(v);
-              w[y][0] = x.x;
-              w[y][1] = x.y;
-              w[y][2 % (D / 32)] = x.z;
-              w[y][3 % (D / 32)] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(v);
-              w[y][0] = x.x;
-              w[y][1] = x.y;
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              pb[k][nb][h] = transpose8x8(kQuant ? pack_f16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1])
+                                                 : pack_bf16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1]));
           }
-          uint32_t bad = 0;
-          if (edge) {
+        }
+        // The slow form of columns dcol(x0 .. x0 + 3, .): products one by one in
+        // fp32, weights of zero left out.  For an infinity or NaN among the values
+        // of a tile that some rows see only in part (0 * infinity would reach rows
+        // that may not see that key), and for value scales too far apart for f16.
+        auto one_by_one = [&](int k, int x0) {
+#pragma unroll 1
+          for (int y = 0; y < 16; ++y)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+            for (int nb = 0; nb < NB; ++nb) {
+              const int src = (y & 7) * 4 + qd;
+              const float f0 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][0] : sc[k][nb][2], src);
+              const float f1 = __shfl_sync(0xffffffffu, y < 8 ? sc[k][nb][1] : sc[k][nb][3], src);
 #pragma unroll
-              for (int z = 0; z < D / 32; ++z) bad |= (w[y][z] & 0x7f7f7f7fu) + 0x01010101u;
-            bad &= 0x80808080u;  // a NaN's code
-          }
-          if (!__any_sync(0xffffffffu, slow[k] || bad)) {
+              for (int x = x0; x < x0 + 4; ++x)
 #pragma unroll
-            for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
-              const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(__byte_perm(w[0][x >> 1], w[1][x >> 1], sel), &a0, &a1);
-              e4m3x4_to_f16(__byte_perm(w[2][x >> 1], w[3][x >> 1], sel), &a2, &a3);
+                for (int e = 0; e < 2; ++e) {
+                  const uint8_t* from = pV + at[k] + v_at(y, dcol(x, e) * ES);
+                  const float v = kQuant ? e4m3x2_to_float2(*from).x
+                                         : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(from)) << 16);
+                  if (f0 != 0.f) acc[nb][x][2 * e] += f0 * v;
+                  if (f1 != 0.f) acc[nb][x][2 * e + 1] += f1 * v;
+                }
+            }
+        };
+        // ---- O^T += V^T P^T
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[k][nb]);
+        for (int k = 0; k < KS; ++k) {
+          if (kQuant) {
+            uint32_t w[4][D / 32];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint8_t* v = pV + at[k] + v_at(2 * qd + (y & 1) + 8 * (y >> 1), rq * (D / 8));
+              if (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(v);
+                w[y][0] = x.x;
+                w[y][1] = x.y;
+                w[y][2 % (D / 32)] = x.z;
+                w[y][3 % (D / 32)] = x.w;
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(v);
+                w[y][0] = x.x;
+                w[y][1] = x.y;
+              }
+            }
+            uint32_t bad = 0;
+            if (edge) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int z = 0; z < D / 32; ++z) bad |= (w[y][z] & 0x7f7f7f7fu) + 0x01010101u;
+              bad &= 0x80808080u;  // a NaN's code
+            }
+            if (!__any_sync(0xffffffffu, slow[k] || bad)) {
+#pragma unroll
+              for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
+                const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(__byte_perm(w[0][x >> 1], w[1][x >> 1], sel), &a0, &a1);
+                e4m3x4_to_f16(__byte_perm(w[2][x >> 1], w[3][x >> 1], sel), &a2, &a3);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[k][nb]);
+              }
+            } else {
+#pragma unroll
+              for (int x0 = 0; x0 < DT; x0 += 4) one_by_one(k, x0);
             }
           } else {
+            const uint32_t from = vaddr + at[k];
 #pragma unroll
-            for (int x0 = 0; x0 < DT; x0 += 4) one_by_one(k, x0);
-          }
-        } else {
-          const uint32_t at = vaddr + kk * PB;
+            for (int x0 = 0; x0 < DT; x0 += 4) {
+              uint32_t a[4][4];
 #pragma unroll
-          for (int x0 = 0; x0 < DT; x0 += 4) {
-            uint32_t a[4][4];
+              for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], (from + part(x0 + x)) ^ (((x0 + x) << 5) & (PB - 1)));
+              bool bad = false;
+              if (edge) {  // value * 0 is a zero for finite values, NaN for others
+                __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f), t = z;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) ldmatrix_x4_trans(a[x], (at + part(x0 + x)) ^ (((x0 + x) << 5) & (PB - 1)));
-            bool bad = false;
-            if (edge) {  // value * 0 is a zero for finite values, NaN for others
-              __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f), t = z;
+                for (int x = 0; x < 16; ++x) t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a[x >> 2][x & 3]), z, t);
+                bad = (*reinterpret_cast<const uint32_t*>(&t) & 0x7fff7fffu) != 0;
+              }
+              if (edge && __any_sync(0xffffffffu, bad)) {
+                one_by_one(k, x0);
+                continue;
+              }
 #pragma unroll
-              for (int x = 0; x < 16; ++x) t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a[x >> 2][x & 3]), z, t);
-              bad = (*reinterpret_cast<const uint32_t*>(&t) & 0x7fff7fffu) != 0;
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x0 + x], a[x][0], a[x][1], a[x][2], a[x][3], pb[k][nb]);
             }
-            if (edge && __any_sync(0xffffffffu, bad)) {
-              one_by_one(k, x0);
-              continue;
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x0 + x], a[x][0], a[x][1], a[x][2], a[x][3], pb[k][nb]);
           }
         }
       }
-    }
-
     };
     if (key0 < free_lo || key0 + TK > free_hi || boxes != all_boxes || p.pad_page != p.c.page_size)
       steps(std::true_type{});
@@ -790,112 +815,177 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG>::kC
       release();
       continue;
     }
-    // ---- the segment's end: the KW warps of a row group join their states in tile n's stage
+    // ---- the segment's end
     fresh = true;
     const int b = t.b, unit = t.unit;
-    const int kh = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - kh * p.nblk) * C::kRows;
+    const int ku = p.nblk == 1 ? unit : unit / p.nblk, row0 = (unit - ku * p.nblk) * C::kRows, kh = ku * HG + hg;
     const bool whole = seg_starts_unit && (flags & kFlagUnitEnd);
     const int slot = 2 * cta + (seg_starts_unit ? 1 : 0);
     if (n + 1 < cnt) load_q(t.next_b, t.next_unit);  // the next unit's queries, on their way meanwhile
+    if (n == cnt - 1 && tid == 0) {
+      int4 s = make_int4(0, 0, 0, 0);
+      if (seg_starts_unit && !(flags & kFlagUnitEnd))  // goes on in the next CTAs
+        s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - group + 1, 0);
+      p.split[cta] = s;
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], o);
-        if (rq == 0) stat[(warp * NB + nb) * 8 + 2 * qd + c] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
-      }
-    float* merge = reinterpret_cast<float*>(smem + st * C::kStageBytes);  // [warps][8 rows][kMergeStride]
+    if constexpr (KW == 1) {  // the warp's rows are its own
+      release();
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      if (!join()) return;  // tile n is read, the block before this one joined
-      float* mine = merge + (warp * 8 + 2 * qd) * C::kMergeStride;
+      for (int nb = 0; nb < NB; ++nb) {
+        const int rloc0 = (rg * NB + nb) * 8;
+        if (row0 + rloc0 >= p.R) break;
+        if (!whole) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (row0 + (rg * NB + nb) * 8 + 2 * qd + c >= p.R) continue;
+          for (int c = 0; c < 2; ++c) {
+            const int rloc = rloc0 + 2 * qd + c;
+            if (row0 + rloc >= p.R) continue;
+            const long long pr = (static_cast<long long>(slot) * HG + hg) * p.prow + rloc;
+            float* o = p.part_o + pr * D;
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
-          if (kQuant) {
-            *reinterpret_cast<float2*>(mine + c * C::kMergeStride + dcol(x, 0)) =
-                make_float2(acc[nb][x][c], acc[nb][x][2 + c]);
-          } else {
-            mine[c * C::kMergeStride + dcol(x, 0)] = acc[nb][x][c];
-            mine[c * C::kMergeStride + dcol(x, 1)] = acc[nb][x][2 + c];
+            for (int x = 0; x < DT; ++x)
+              if (kQuant) {
+                *reinterpret_cast<float2*>(o + dcol(x, 0)) = make_float2(acc[nb][x][c], acc[nb][x][2 + c]);
+              } else {
+                o[dcol(x, 0)] = acc[nb][x][c];
+                o[dcol(x, 1)] = acc[nb][x][2 + c];
+              }
+            if (rq == 0) p.part_m[pr] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
           }
-      }
-      if (!join()) return;
-      constexpr int LPR = D / 4, RPP = 32 * kPagedWarps / LPR;  // threads of a row, rows of a pass
-      const int col = tid % LPR * 4;
-#pragma unroll
-      for (int it = 0; it < RG * 8 / RPP; ++it) {
-        const int rr = tid / LPR + it * RPP, g = rr >> 3, r8 = rr & 7;  // row r8 of group g
-        const int rloc = (g * NB + nb) * 8 + r8, r = row0 + rloc;
-        if (r >= p.R) continue;
-        float mt = -INFINITY, vt = 0.f, lt = 0.f;
-        float4 st[KW], a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          st[w] = stat[((g * KW + w) * NB + nb) * 8 + r8];
-          mt = fmaxf(mt, st[w].x);
-          vt = fmaxf(vt, st[w].z);
+          continue;
         }
-        const float vti = __uint_as_float((254u << 23) - __float_as_uint(vt));
+        float inv[2];
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          float f = st[w].x == -INFINITY ? (st[w].y == 0.f ? 0.f : 1.f) : exp2_fast(st[w].x - mt);
-          lt += f * st[w].y;
-          if (kQuant) f *= st[w].z * vti;
-          const float4 v = *reinterpret_cast<const float4*>(merge + ((g * KW + w) * 8 + r8) * C::kMergeStride + col);
-          if (f != 0.f) {
-            a.x += f * v.x;
-            a.y += f * v.y;
-            a.z += f * v.z;
-            a.w += f * v.w;
-          }
-        }
-        if (whole) {
+        for (int c = 0; c < 2; ++c) {
+          inv[c] = l[nb][c] == 0.f ? 0.f : 1.f / l[nb][c];
+          const int r = row0 + rloc0 + 2 * qd + c;
+          if (r >= p.R) continue;
           const int hq = p.Nq == 1 ? r : r / p.Nq, h = kh * p.g + hq, i = r - hq * p.Nq;
-          const float inv = lt == 0.f ? 0.f : 1.f / lt, u = kQuant ? vt : 1.f;
-          *reinterpret_cast<uint2*>(p.o + 2 * (p.so.row(b, h, i) + col)) =
-              make_uint2(pack_bf16(a.x * inv * u, a.y * inv * u), pack_bf16(a.z * inv * u, a.w * inv * u));
-          if (col == 0)
+          if (rq == 0)
             p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] =
-                lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
-        } else {
-          const long long pr = static_cast<long long>(slot) * p.prow + rloc;
-          *reinterpret_cast<float4*>(p.part_o + pr * D + col) = a;
-          if (col == 0) p.part_m[pr] = make_float4(mt, lt, vt, 0.f);
+                l[nb][c] == 0.f ? -INFINITY : (m[nb][c] + log2f(l[nb][c])) * 0.69314718055994531f;
+          if (kQuant) {  // D / 8 columns in line
+            const float u = vref[nb][c];
+            uint32_t w[DT];
+#pragma unroll
+            for (int x = 0; x < DT; ++x) w[x] = pack_bf16(acc[nb][x][c] * inv[c] * u, acc[nb][x][2 + c] * inv[c] * u);
+            uint4* o = reinterpret_cast<uint4*>(p.o + 2 * (p.so.row(b, h, i) + rq * (D / 8)));
+#pragma unroll
+            for (int x = 0; x < DT; x += 4) o[x / 4] = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+          }
+        }
+        if (!kQuant) {  // 8 x 8 blocks of columns and rows, turned so that a lane has two columns of row rq
+          const int r = row0 + rloc0 + rq;
+          const int hq = p.Nq == 1 ? r : r / p.Nq, h = kh * p.g + hq, i = r - hq * p.Nq;
+          uint32_t* o = reinterpret_cast<uint32_t*>(p.o + 2 * (r < p.R ? p.so.row(b, h, i) : 0)) + qd;
+#pragma unroll
+          for (int x = 0; x < DT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t w = transpose8x8(pack_bf16(acc[nb][x][2 * e] * inv[0], acc[nb][x][2 * e + 1] * inv[1]));
+              if (r < p.R) o[8 * x + 4 * e] = w;
+            }
         }
       }
-    }
-    if (n == cnt - 1 && tid == 0) {
-      int4 s = make_int4(0, 0, 0, 0);
-      if (seg_starts_unit && !(flags & kFlagUnitEnd)) {  // goes on in the next CTAs
-        s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - group + 1, 0);
+    } else {
+      // the KW warps of a row group join their states in tile n's stage
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (rq == 0) stat[(warp * NB + nb) * 8 + 2 * qd + c] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
+        }
+      float* merge = reinterpret_cast<float*>(smem + st * C::kStageBytes);  // [warps][8 rows][kMergeStride]
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        if (!join()) return;  // tile n is read, the block before this one joined
+        float* mine = merge + (warp * 8 + 2 * qd) * C::kMergeStride;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (row0 + (rg * NB + nb) * 8 + 2 * qd + c >= p.R) continue;
+#pragma unroll
+          for (int x = 0; x < DT; ++x)
+            if (kQuant) {
+              *reinterpret_cast<float2*>(mine + c * C::kMergeStride + dcol(x, 0)) =
+                  make_float2(acc[nb][x][c], acc[nb][x][2 + c]);
+            } else {
+              mine[c * C::kMergeStride + dcol(x, 0)] = acc[nb][x][c];
+              mine[c * C::kMergeStride + dcol(x, 1)] = acc[nb][x][2 + c];
+            }
+        }
+        if (!join()) return;
+        constexpr int LPR = D / 4, RPP = 32 * kPagedWarps / LPR;  // threads of a row, rows of a pass
+        const int col = tid % LPR * 4;
+#pragma unroll
+        for (int it = 0; it < RG * 8 / RPP; ++it) {
+          const int rr = tid / LPR + it * RPP, g = rr >> 3, r8 = rr & 7;  // row r8 of group g
+          const int rloc = (g * NB + nb) * 8 + r8, r = row0 + rloc;
+          if (r >= p.R) continue;
+          float mt = -INFINITY, vt = 0.f, lt = 0.f;
+          float4 st[KW], a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            st[w] = stat[((g * KW + w) * NB + nb) * 8 + r8];
+            mt = fmaxf(mt, st[w].x);
+            vt = fmaxf(vt, st[w].z);
+          }
+          const float vti = __uint_as_float((254u << 23) - __float_as_uint(vt));
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            float f = st[w].x == -INFINITY ? (st[w].y == 0.f ? 0.f : 1.f) : exp2_fast(st[w].x - mt);
+            lt += f * st[w].y;
+            if (kQuant) f *= st[w].z * vti;
+            const float4 v = *reinterpret_cast<const float4*>(merge + ((g * KW + w) * 8 + r8) * C::kMergeStride + col);
+            if (f != 0.f) {
+              a.x += f * v.x;
+              a.y += f * v.y;
+              a.z += f * v.z;
+              a.w += f * v.w;
+            }
+          }
+          if (whole) {
+            const int hq = p.Nq == 1 ? r : r / p.Nq, h = kh * p.g + hq, i = r - hq * p.Nq;
+            const float inv = lt == 0.f ? 0.f : 1.f / lt, u = kQuant ? vt : 1.f;
+            *reinterpret_cast<uint2*>(p.o + 2 * (p.so.row(b, h, i) + col)) =
+                make_uint2(pack_bf16(a.x * inv * u, a.y * inv * u), pack_bf16(a.z * inv * u, a.w * inv * u));
+            if (col == 0)
+              p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] =
+                  lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
+          } else {
+            const long long pr = static_cast<long long>(slot) * p.prow + rloc;
+            *reinterpret_cast<float4*>(p.part_o + pr * D + col) = a;
+            if (col == 0) p.part_m[pr] = make_float4(mt, lt, vt, 0.f);
+          }
+        }
       }
-      p.split[cta] = s;
+      fence_proxy_async_smem();  // the stage was written here; the TMA writes it next
+      release();
     }
-    fence_proxy_async_smem();  // the stage was written here; the TMA writes it next
-    release();
   }
 }
 
 // Joins the partials of the units that several CTAs share: block (c, y) the
-// unit that starts in CTA c, 8 rows of it, a warp each.  Partial 0 is CTA c's
+// unit that starts in CTA c, 8 rows of its heads, a warp each.  Partial 0 is CTA c's
 // second slot, the others are the lane's following CTAs' first.
 template <int D, bool kQuant>
-__global__ void __launch_bounds__(32 * kPagedCombineRows) paged_combine_kernel(const PagedParams p, int rows_unit) {
+__global__ void __launch_bounds__(32 * kPagedCombineRows)
+    paged_combine_kernel(const PagedParams p, int rows_unit, int heads_unit) {
   constexpr int E = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 s = p.split[blockIdx.x];
   const int parts = s.z;
   if (parts == 0) return;
   const int lane = threadIdx.x & 31;
-  const int rloc = blockIdx.y * kPagedCombineRows + (threadIdx.x >> 5);
-  const int kh = s.y / p.nblk, r = (s.y % p.nblk) * rows_unit + rloc;
-  if (rloc >= rows_unit || r >= p.R) return;
+  const int row = blockIdx.y * kPagedCombineRows + (threadIdx.x >> 5), hg = row / p.prow, rloc = row - hg * p.prow;
+  const int ku = s.y / p.nblk, kh = ku * heads_unit + hg, r = (s.y - ku * p.nblk) * rows_unit + rloc;
+  if (hg >= heads_unit || r >= p.R) return;
   auto at = [&](int i) {
-    return (static_cast<long long>(2) * (blockIdx.x + i * p.lanes) + (i == 0 ? 1 : 0)) * p.prow + rloc;
+    return ((static_cast<long long>(2) * (blockIdx.x + i * p.lanes) + (i == 0 ? 1 : 0)) * heads_unit + hg) * p.prow + rloc;
   };
   float m = -INFINITY, l = 0.f, u = 0x1p-126f, acc[E];  // u: the accumulators' unit, the largest so far
 #pragma unroll
