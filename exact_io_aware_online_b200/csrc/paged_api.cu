@@ -214,8 +214,17 @@ PagedOffsets paged_offsets(int rows, int d) {
 }
 
 int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }  // rows of a kv head in a unit
-// kv heads of a unit: as many as leave each warp rows of its own, where they divide Hkv
-int paged_heads(int R, int Hkv) { return R <= 8 && Hkv % 4 == 0 ? 4 : R > 8 && R <= 16 && Hkv % 2 == 0 ? 2 : 1; }
+// kv heads of a unit: as many as leave each warp rows of its own, where they
+// divide Hkv.  One for few sequences, whose units all CTAs would share (one
+// token over 4000 in bf16, B = 1: 23 us against 29 us with four; B = 8, 32768:
+// the same), and where a tile of 32 KB would be 16 keys (rows of 256 bytes: 64
+// ragged sequences 125 us against 130 us; rows of 128 bytes, pages of 16: 107 us
+// with four against 123 us).
+int paged_heads(int B, int R, int Hkv, int row_bytes) {
+  if (B * static_cast<long long>(Hkv) < 64) return 1;
+  if (R <= 8 && row_bytes < 256 && Hkv % 4 == 0) return 4;
+  return R > 8 && R <= 16 && Hkv % 2 == 0 ? 2 : 1;
+}
 
 template <int D, bool kQuant, int NB, int RG, int HG>
 fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStream_t st) {
@@ -236,6 +245,8 @@ fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStrea
   if (!page_map(&mk, cache->k_pages, p.c, D, kQuant, 1 << p.box_log, HG) ||
       !page_map(&mv, cache->v_pages, p.c, D, kQuant, 1 << p.box_log, HG))
     return FA_ERR_CUDA;
+  p.scale_rows = kQuant && (HG == 1 || p.c.scales.h == 1) && p.c.scales.n % HG == 0 && p.c.scales.b % HG == 0 &&
+                 ((reinterpret_cast<uintptr_t>(p.c.ks) | reinterpret_cast<uintptr_t>(p.c.vs)) & (4 * HG - 1)) == 0;
   // lanes: the largest divisor of a sequence's units that leaves at most one CTA in sixteen without work
   const int units = p.c.Hkv / HG * p.nblk, most = 148 * C::kCtas;
   p.lanes = std::min(units, most);
@@ -248,13 +259,17 @@ fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStrea
   const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles * (units / p.lanes)));
   const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, mk, mv, p);
   if (s != FA_OK) return s;
-  const dim3 grid(ctas, (HG * p.prow + fa::kPagedCombineRows - 1) / fa::kPagedCombineRows);
-  return launch(fa::paged_combine_kernel<D, kQuant>, grid, dim3(32 * fa::kPagedCombineRows), 0, st, true, p, C::kRows, HG);
+  // four warps a row where there are few rows (a wave of warps, and few blocks without work)
+  const bool few = HG * p.prow <= 8 && static_cast<long long>(p.c.B) * p.H * p.Nq <= 148 * 16;
+  const int rows = fa::kPagedCombineWarps / (few ? 4 : 1);
+  const dim3 grid(ctas, (HG * p.prow + rows - 1) / rows), block(32 * fa::kPagedCombineWarps);
+  return few ? launch(fa::paged_combine_kernel<D, kQuant, 4>, grid, block, 0, st, true, p, C::kRows, HG)
+             : launch(fa::paged_combine_kernel<D, kQuant, 1>, grid, block, 0, st, true, p, C::kRows, HG);
 }
 
 template <int D, bool kQuant>
 fa_status launch_paged_rows(const fa_paged_cache* cache, const fa::PagedParams& p, cudaStream_t st) {
-  const int heads = paged_heads(p.R, p.c.Hkv);
+  const int heads = paged_heads(p.c.B, p.R, p.c.Hkv, kQuant ? D : 2 * D);
   switch (paged_rows(p.R)) {
     case 8:
       return heads == 4 ? launch_paged<D, kQuant, 1, 1, 4>(cache, p, st) : launch_paged<D, kQuant, 1, 1, 1>(cache, p, st);
@@ -303,7 +318,7 @@ size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d) {
   if (!paged_sizes_ok(B, H, Hkv, Nq) || (d != 64 && d != 128)) return 0;
   const long long R = static_cast<long long>(H / Hkv) * Nq;
   const int r = static_cast<int>(std::min(R, 64LL));
-  return paged_offsets(paged_heads(r, Hkv) * r, d).bytes;
+  return paged_offsets(paged_heads(B, r, Hkv, d) * r, d).bytes;  // of a quantised cache: the most heads
 }
 
 fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,
@@ -337,15 +352,15 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   const int block = paged_rows(p.R);
   p.nblk = (p.R + block - 1) / block;
   p.prow = std::min(p.R, block);
+  const bool quant = cache->dtype == FA_CACHE_E4M3;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const PagedOffsets at = paged_offsets(paged_heads(p.R, Hkv) * p.prow, d);
+  const PagedOffsets at = paged_offsets(paged_heads(B, p.R, Hkv, quant ? d : 2 * d) * p.prow, d);
   p.split = reinterpret_cast<int4*>(ws);
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
   p.pad_page = (cache->page_size + 7) & ~7;
   magic(p.pad_page, &p.pad_mul, &p.pad_shift);
   if (static_cast<long long>(cache->max_pages) * p.pad_page > (1LL << 30)) return FA_ERR_UNSUPPORTED;  // padded positions are 32-bit too
-  const bool quant = cache->dtype == FA_CACHE_E4M3;
   if (d == 64) return quant ? launch_paged_rows<64, true>(cache, p, st) : launch_paged_rows<64, false>(cache, p, st);
   return quant ? launch_paged_rows<128, true>(cache, p, st) : launch_paged_rows<128, false>(cache, p, st);
 }

@@ -46,7 +46,7 @@ namespace fa {
 constexpr int kPagedWarps = 4;      // that compute; one more loads
 constexpr int kPagedThreads = 32 * (kPagedWarps + 1);
 constexpr int kPagedMaxCtas = 444;  // three on each of 148 SMs
-constexpr int kPagedCombineRows = 8;
+constexpr int kPagedCombineWarps = 8;
 
 struct PagedParams {
   CacheParams c;
@@ -63,6 +63,7 @@ struct PagedParams {
   uint32_t pad_mul;  // pos / pad_page, as CacheParams::page_mul
   int pad_shift;
   int box_log;     // log2 of the tokens of a TMA box: 3 to 5
+  int scale_rows;  // the scales of a unit's kv heads lie in line, aligned to their size
   int prow;        // rows of a partial: min(R, rows of a unit)
   float* part_o;   // [2 * G][kv heads of a unit][prow][D]
   float4* part_m;  // [2 * G][kv heads of a unit][prow]: m, l, unit of the accumulator
@@ -93,9 +94,10 @@ struct PagedCfg {
                 "the warps' accumulators are joined in a stage");
 };
 
-// 4 bytes to shared memory, zero when !on.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+// N = 4, 8 or 16 bytes to shared memory, zeros when !on.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
 }
 // The barrier counts an arrival once this thread's cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -146,6 +148,11 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+// What a state (m, l) counts for in one whose maximum is mt.  A state without a
+// key has no weight; one of NaN alone (its maximum still -infinity) passes on.
+__device__ __forceinline__ float paged_weight(float m, float l, float mt) {
+  return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - mt);
 }
 // Four e4m3 codes (the lowest first) as f16 numbers (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t* lo, uint32_t* hi) {
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
       }
       if (kQuant) {
         const long long at = on ? p.c.scales.row(cur.page, kh, cur.slot) : -1;
-        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes) + lane * 4;  // [heads][keys]
+        const uint32_t to = smem_u32(dst + 2 * C::kTileBytes);
         constexpr int TL = TK < 32 ? 32 : TK;  // a head's entries, in groups of 32
         long long off[TL / 32];
         bool here[TL / 32];
@@ -411,15 +418,27 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
           here[i] = off[i] >= 0 && slot < p.c.page_size;
           off[i] += in * p.c.scales.n;
         }
+        if (TK >= 32 || lane < TK) {
+          if (p.scale_rows) {  // [keys][heads]: the unit's heads in one copy
 #pragma unroll
-        for (int h = 0; h < HG; ++h)
+            for (int i = 0; i < TL / 32; ++i) {
+              const uint32_t at = to + (i * 32 + lane) * HG * 4;
+              const long long from = here[i] ? off[i] : 0;
+              cp_async<HG * 4>(at, p.c.ks + from, here[i]);
+              cp_async<HG * 4>(at + C::kScaleBytes, p.c.vs + from, here[i]);
+            }
+          } else {  // [heads][keys]
 #pragma unroll
-          for (int i = 0; i < TL / 32; ++i) {
-            if (TK < 32 && lane >= TK) break;
-            const long long from = here[i] ? off[i] + h * p.c.scales.h : 0;
-            cp_async4(to + (h * TK + i * 32) * 4, p.c.ks + from, here[i]);
-            cp_async4(to + (h * TK + i * 32) * 4 + C::kScaleBytes, p.c.vs + from, here[i]);
+            for (int h = 0; h < HG; ++h)
+#pragma unroll
+              for (int i = 0; i < TL / 32; ++i) {
+                const uint32_t at = to + (h * TK + i * 32 + lane) * 4;
+                const long long from = here[i] ? off[i] + h * p.c.scales.h : 0;
+                cp_async<4>(at, p.c.ks + from, here[i]);
+                cp_async<4>(at + C::kScaleBytes, p.c.vs + from, here[i]);
+              }
           }
+        }
         cp_async_arrive(full + st);
       }
       cur = next;
@@ -491,6 +510,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     return byte / PB * HG * TK * PB + (key & 7) * PB + (key >> 3) * half + ((((byte % PB) >> 4) ^ swz(key)) << 4) + (byte & 15);
   };
 
+  const int scl_step = p.scale_rows ? HG : 1, scl_at = p.scale_rows ? rq * HG + hg : hg * TK + rq;
+
   load_q(fb, fu * p.lanes + ulane);
   for (int n = 0; n < cnt; ++n) {
     if (!__all_sync(0xffffffffu, mbar_wait(full + st, ph, abort))) return;
@@ -551,7 +572,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 
     const uint8_t* pV = smem + st * C::kStageBytes + C::kTileBytes;
     const uint32_t kaddr = smem_u32(smem + st * C::kStageBytes) + kat, vaddr = smem_u32(pV) + vat;
-    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes) + hg * TK;  // K's, HG * TK further V's
+    const float* scl = reinterpret_cast<const float*>(pV + C::kTileBytes) + scl_at;  // K's, HG * TK further V's
     // the steps of a tile; kEdge: some row may not see some key of it
     auto steps = [&](auto edge_tile) {
       constexpr bool edge = decltype(edge_tile)::value;
@@ -593,8 +614,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float ks = kQuant ? scl[kb + 16 * k + 8 * h + rq] : 1.f;
-            vs[k][h] = kQuant ? scl[HG * TK + kb + 16 * k + 8 * h + rq] : 1.f;
+            const float ks = kQuant ? scl[(kb + 16 * k + 8 * h) * scl_step] : 1.f;
+            vs[k][h] = kQuant ? scl[HG * TK + (kb + 16 * k + 8 * h) * scl_step] : 1.f;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -937,7 +958,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
           const float vti = __uint_as_float((254u << 23) - __float_as_uint(vt));
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
-            float f = st[w].x == -INFINITY ? (st[w].y == 0.f ? 0.f : 1.f) : exp2_fast(st[w].x - mt);
+            float f = paged_weight(st[w].x, st[w].y, mt);
             lt += f * st[w].y;
             if (kQuant) f *= st[w].z * vti;
             const float4 v = *reinterpret_cast<const float4*>(merge + ((g * KW + w) * 8 + r8) * C::kMergeStride + col);
@@ -970,75 +991,115 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 }
 
 // Joins the partials of the units that several CTAs share: block (c, y) the
-// unit that starts in CTA c, 8 rows of its heads, a warp each.  Partial 0 is CTA c's
-// second slot, the others are the lane's following CTAs' first.
-template <int D, bool kQuant>
-__global__ void __launch_bounds__(32 * kPagedCombineRows)
+// unit that starts in CTA c, 8 / CW rows of its heads.  Partial 0 is CTA c's
+// second slot, the others are the lane's following CTAs' first.  CW warps take
+// every CW-th partial of a row each: what bounds this is the latency of the
+// loads, of which a warp has eight on their way.
+template <int D, bool kQuant, int CW>
+__global__ void __launch_bounds__(32 * kPagedCombineWarps)
     paged_combine_kernel(const PagedParams p, int rows_unit, int heads_unit) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kRows = kPagedCombineWarps / CW;
+  __shared__ float4 stat[kRows][CW];
+  __shared__ float part[CW > 1 ? kRows : 1][CW][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 s = p.split[blockIdx.x];
   const int parts = s.z;
   if (parts == 0) return;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kPagedCombineRows + (threadIdx.x >> 5), hg = row / p.prow, rloc = row - hg * p.prow;
+  const int lane = threadIdx.x & 31, brow = threadIdx.x / (32 * CW), cw = (threadIdx.x >> 5) % CW;
+  const int row = blockIdx.y * kRows + brow, hg = row / p.prow, rloc = row - hg * p.prow;
   const int ku = s.y / p.nblk, kh = ku * heads_unit + hg, r = (s.y - ku * p.nblk) * rows_unit + rloc;
-  if (hg >= heads_unit || r >= p.R) return;
-  auto at = [&](int i) {
-    return ((static_cast<long long>(2) * (blockIdx.x + i * p.lanes) + (i == 0 ? 1 : 0)) * heads_unit + hg) * p.prow + rloc;
-  };
+  const bool on = hg < heads_unit && r < p.R;
   float m = -INFINITY, l = 0.f, u = 0x1p-126f, acc[E];  // u: the accumulators' unit, the largest so far
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  constexpr int kAhead = 8;
-  float v[kAhead][E];
-  auto load = [&](int i, int cnt) {
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      const float* src = p.part_o + at(i + y) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        float2 f = make_float2(0.f, 0.f);
-        if (y < cnt) f = *reinterpret_cast<const float2*>(src + e);
-        v[y][e] = f.x;
-        v[y][e + 1] = f.y;
-      }
-    }
-  };
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const int cnt = min(32, parts - i0);
-    load(i0, cnt);  // on their way while the weights are formed
-    float4 st = make_float4(-INFINITY, 0.f, 0x1p-126f, 0.f);
-    if (i0 + lane < parts) st = p.part_m[at(i0 + lane)];
-    float mn = fmaxf(m, st.x), un = fmaxf(u, st.z);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      un = fmaxf(un, __shfl_xor_sync(0xffffffffu, un, o));
-    }
-    const float ui = __uint_as_float((254u << 23) - __float_as_uint(un));
-    float old = m == -INFINITY ? 0.f : exp2_fast(m - mn);
-    float w = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : exp2_fast(st.x - mn);
-    float ls = w == 0.f ? 0.f : w * st.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-    l = l * old + ls;
-    old *= u * ui;
-    w *= st.z * ui;
-    m = mn;
-    u = un;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= old;
-    for (int i = 0; i < cnt; i += kAhead) {
-      if (i != 0) load(i0 + i, cnt - i);
+  if (on) {
+    const int mine = (parts - cw + CW - 1) / CW;  // partials cw, cw + CW, ...
+    auto at = [&](int i) {
+      i = cw + i * CW;
+      return ((static_cast<long long>(2) * (blockIdx.x + i * p.lanes) + (i == 0 ? 1 : 0)) * heads_unit + hg) * p.prow + rloc;
+    };
+    constexpr int kAhead = 8;
+    float v[kAhead][E];
+    auto load = [&](int i, int cnt) {
 #pragma unroll
       for (int y = 0; y < kAhead; ++y) {
-        const float wi = __shfl_sync(0xffffffffu, w, (i + y) & 31);
-        if (i + y < cnt && wi != 0.f)
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += wi * v[y][e];
+        for (int e = 0; e < E; ++e) v[y][e] = 0.f;
+        if (y < cnt) {
+          const float* src = p.part_o + at(i + y) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(src + e);
+            v[y][e] = f.x;
+            v[y][e + 1] = f.y;
+          }
+        }
+      }
+    };
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      const int cnt = min(32, mine - i0);
+      load(i0, cnt);  // on their way while the weights are formed
+      float4 st = make_float4(-INFINITY, 0.f, 0x1p-126f, 0.f);
+      if (lane < cnt) st = p.part_m[at(i0 + lane)];
+      float mn = fmaxf(m, st.x), un = fmaxf(u, st.z);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        un = fmaxf(un, __shfl_xor_sync(0xffffffffu, un, o));
+      }
+      const float ui = __uint_as_float((254u << 23) - __float_as_uint(un));
+      float old = paged_weight(m, l, mn), w = paged_weight(st.x, st.y, mn);
+      float ls = w == 0.f ? 0.f : w * st.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      l = l * old + ls;
+      old *= u * ui;
+      w *= st.z * ui;
+      m = mn;
+      u = un;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= old;
+      for (int i = 0; i < cnt; i += kAhead) {
+        if (i != 0) load(i0 + i, cnt - i);
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+          const float wi = __shfl_sync(0xffffffffu, w, (i + y) & 31);
+          if (i + y < cnt && wi != 0.f)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += wi * v[y][e];
+        }
       }
     }
+    if (CW > 1) {
+      if (lane == 0) stat[brow][cw] = make_float4(m, l, u, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[CW > 1 ? brow : 0][cw][lane * E + e] = acc[e];
+    }
+  }
+  if (CW > 1) {
+    __syncthreads();
+    if (!on || cw != 0) return;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) {
+      m = fmaxf(m, stat[brow][w].x);
+      u = fmaxf(u, stat[brow][w].z);
+    }
+    const float ui = __uint_as_float((254u << 23) - __float_as_uint(u));
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) {
+      const float4 st = stat[brow][w];
+      float f = paged_weight(st.x, st.y, m);
+      if (f == 0.f) continue;
+      l += f * st.y;
+      f *= st.z * ui;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += f * part[CW > 1 ? brow : 0][w][lane * E + e];
+    }
+  } else if (!on) {
+    return;
   }
   const int h = kh * p.g + r / p.Nq, i = r % p.Nq;
   const float inv = l == 0.f ? 0.f : 1.f / l;
