@@ -140,7 +140,7 @@ def _on(device, fn, *args):
     the stream it is given and rejects a stream of another device than the
     current one."""
     import torch
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -603,19 +603,18 @@ def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
     describes them (it holds pointers only: the tensors stay the caller's), their
     device, and the numbers of sequences, kv heads and head_dim."""
     import torch
-    if k_pages.dim() != 4:
+    dtype, shape, st, at = k_pages.dtype, k_pages.shape, k_pages.stride(), k_pages.get_device()
+    if len(shape) != 4:
         raise ValueError("k_pages, v_pages must be 4-D [pages, kv heads, page size, head_dim]")
-    dtype = k_pages.dtype
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         code = FA_CACHE_BF16
-    elif dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         code = FA_CACHE_E4M3
     else:
         raise TypeError(f"k_pages: unsupported dtype {dtype} (bfloat16 or float8_e4m3fn)")
-    shape, st = k_pages.shape, k_pages.stride()
     if v_pages.shape != shape:
         raise ValueError(f"v_pages: shape {tuple(v_pages.shape)}, expected {tuple(shape)}")
-    if v_pages.dtype != dtype:
+    if v_pages.dtype is not dtype:
         raise TypeError(f"v_pages: dtype {v_pages.dtype}, expected {dtype}")
     if v_pages.stride() != st or st[3] != 1:
         raise ValueError("k_pages, v_pages must have the same strides and a contiguous last axis")
@@ -623,53 +622,57 @@ def _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale):
     table_shape, table_stride = page_table.shape, page_table.stride()
     if len(table_shape) != 2 or seqlens.shape != table_shape[:1]:
         raise ValueError("page_table must be [sequences, pages of a sequence] and seqlens [sequences]")
-    if page_table.dtype != torch.int32 or seqlens.dtype != torch.int32:
+    if page_table.dtype is not torch.int32 or seqlens.dtype is not torch.int32:
         raise TypeError("page_table and seqlens must be int32")
     B, M = table_shape
     if (M > 1 and table_stride[1] != 1) or (B > 1 and (table_stride[0] < M or seqlens.stride(0) != 1)):
         raise ValueError("page_table must have contiguous rows that do not overlap, and seqlens must be contiguous")
-    tensors = [(v_pages, "v_pages"), (page_table, "page_table"), (seqlens, "seqlens")]
     ks = vs = s0 = s1 = s2 = 0
     if code == FA_CACHE_BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale, v_scale belong to a float8_e4m3fn cache")
     else:
+        want = shape[:3]
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None or t.shape != shape[:3] or t.dtype != torch.float32:
-                raise ValueError(f"{name}: must be a float32 tensor of shape {tuple(shape[:3])}")
+            if t is None or t.shape != want or t.dtype is not torch.float32:
+                raise ValueError(f"{name}: must be a float32 tensor of shape {tuple(want)}")
+            if t.get_device() != at:
+                raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {k_pages.device})")
         s0, s1, s2 = ss = k_scale.stride()
         if v_scale.stride() != ss:
             raise ValueError("k_scale, v_scale must have the same strides")
-        tensors += [(k_scale, "k_scale"), (v_scale, "v_scale")]
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    if not k_pages.is_cuda:
-        raise ValueError(f"k_pages: must be on a CUDA device, got {k_pages.device}")
-    at = k_pages.get_device()
-    for t, name in tensors:
-        if t.get_device() != at:
-            raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {k_pages.device})")
+    device = k_pages.device
+    if device.type != "cuda":
+        raise ValueError(f"k_pages: must be on a CUDA device, got {device}")
+    if v_pages.get_device() != at or page_table.get_device() != at or seqlens.get_device() != at:
+        raise ValueError(f"v_pages, page_table, seqlens: must be on the CUDA device of k_pages, got {v_pages.device}, "
+                         f"{page_table.device}, {seqlens.device} (k_pages: {device})")
     return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, page_table.data_ptr(), seqlens.data_ptr(), st[0],
-                       st[1], st[2], s0, s1, s2, table_stride[0], B, Hkv, d, P, page, M, code), k_pages.device, B, Hkv, d
+                       st[1], st[2], s0, s1, s2, table_stride[0], B, Hkv, d, P, page, M, code), device, B, Hkv, d
 
 
 def _move_args(B, Hkv, d, k, v, cu_seqlens, T, device):
     """Checks the packed tokens k, v [T, Hkv, d] (d contiguous) and the device
     offsets of cache_write() / cache_read(); their two fa_strides."""
     import torch
-    shape, at = (T, Hkv, d), device.index
+    shape, at, strides = (T, Hkv, d), device.index, []
     for t, name in ((k, "k"), (v, "v")):
         if t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
-        if t.stride(2) != 1:
+        st = t.stride()
+        if st[2] != 1:
             raise ValueError(f"{name}: must have a contiguous last axis")
         if t.get_device() != at:
             raise ValueError(f"{name}: must be on the CUDA device of k_pages, got {t.device} (k_pages: {device})")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (B + 1,) or cu_seqlens.get_device() != at \
+        strides.append(st)
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.shape != (B + 1,) or cu_seqlens.get_device() != at \
             or cu_seqlens.stride(0) != 1:
         raise TypeError(f"cu_seqlens must be a contiguous int32 tensor of {B + 1} values on the device of k_pages")
-    return _pack_two(1, k.stride(1), k.stride(0), 1, v.stride(1), v.stride(0))
+    (kn, kh, _), (vn, vh, _) = strides
+    return _pack_two(1, kh, kn, 1, vh, vn)
 
 
 def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale=None, v_scale=None):
@@ -733,7 +736,7 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
     _, H, Nq, _ = shape
     if shape[0] != B or shape[3] != d:
         raise ValueError(f"q: shape {tuple(shape)}, expected {B} sequences of head_dim {d}")
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q: dtype {q.dtype}, expected torch.bfloat16")
     if q.get_device() != device.index:
         raise ValueError(f"q: must be on the CUDA device of k_pages, got {q.device} (k_pages: {device})")

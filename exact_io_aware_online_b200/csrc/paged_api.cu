@@ -256,9 +256,16 @@ fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStrea
   const double tiles = static_cast<double>((cap + C::kTile - 1) / C::kTile) * p.c.B;  // of one unit of each sequence
   // tiles are counted in 32 bits: those of a CTA, and of all sequences
   if (tiles > 2e9 || tiles * units / most > 1e9) return FA_ERR_UNSUPPORTED;
+  // tiles of a unit at most: of the table's tokens, or of a window's and the pages and boxes it cuts
+  long long keys = cap;
+  if (p.window >= 0) {
+    const long long seen = static_cast<long long>(p.window) + p.Nq;
+    keys = std::min(cap, (seen + 2 * p.c.page_size - 2) / p.c.page_size * p.pad_page);
+  }
+  p.whole = (keys + C::kTile - 1) / C::kTile <= fa::kPagedWhole;
   const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles * (units / p.lanes)));
   const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, mk, mv, p);
-  if (s != FA_OK) return s;
+  if (s != FA_OK || p.whole) return s;
   // four warps a row where there are few rows (a wave of warps, and few blocks without work)
   const bool few = HG * p.prow <= 8 && static_cast<long long>(p.c.B) * p.H * p.Nq <= 148 * 16;
   const int rows = fa::kPagedCombineWarps / (few ? 4 : 1);

@@ -29,7 +29,9 @@
 // join their states at a unit's end.  A unit that lies in one share is finished
 // by its CTA; one that several share leaves a partial (m, l,
 // accumulator) per CTA -- at most two per CTA, so the workspace does not grow
-// with the batch -- for paged_combine_kernel.
+// with the batch -- for paged_combine_kernel.  Where no unit can have more than
+// kPagedWhole tiles, none is shared: its group is the one its first tile falls
+// to, and there is nothing to combine.
 //
 // Positions inside the kernel are padded: a page counts as page_size rounded up
 // to 8 tokens, so that a box never spans two pages; the slots that do not exist
@@ -47,6 +49,7 @@ constexpr int kPagedWarps = 4;      // that compute; one more loads
 constexpr int kPagedThreads = 32 * (kPagedWarps + 1);
 constexpr int kPagedMaxCtas = 444;  // three on each of 148 SMs
 constexpr int kPagedCombineWarps = 8;
+constexpr int kPagedWhole = 4;
 
 struct PagedParams {
   CacheParams c;
@@ -59,6 +62,7 @@ struct PagedParams {
   int causal, window;
   int R, nblk;     // rows of a kv head (g * Nq), blocks they make
   int lanes;       // CTAs of a group: a divisor of a sequence's units
+  int whole;       // no unit is shared
   int pad_page;    // page_size rounded up to a multiple of 8
   uint32_t pad_mul;  // pos / pad_page, as CacheParams::page_mul
   int pad_shift;
@@ -148,6 +152,15 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+// mbar_wait() that first polls without a look at the clock and the limit (in
+// global memory): most waits here are shorter than that.
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(a, parity)) return true;
+  return mbar_wait(bar, parity, abort);
 }
 // What a state (m, l) counts for in one whose maximum is mt.  A state without a
 // key has no weight; one of NaN alone (its maximum still -infinity) passes on.
@@ -247,7 +260,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     if (w < warp) before += red[w];
     sum += red[w];
   }
-  const int c0 = (sum >> 32) * U >= 2LL * groups ? 1 : 0;  // few tiles: one for each CTA
+  const int c0 = p.whole || (sum >> 32) * U >= 2LL * groups ? 1 : 0;  // few tiles: one for each CTA
   auto cost = [&](long long x) { return ((x >> 32) + (x & 0xffffffffLL) * c0) * U; };
   const long long W = cost(sum);
   // groups with a share: c0 + 1 or more, so that each holds a tile
@@ -266,7 +279,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     }
   }
   if (group >= G) {
-    if (tid == 0) p.split[cta] = make_int4(0, 0, 0, 0);
+    if (tid == 0 && !p.whole) p.split[cta] = make_int4(0, 0, 0, 0);
     return;
   }
 
@@ -286,8 +299,17 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         continue;
       }
       const long long in = at - cost(from);
-      const int u = static_cast<int>(in / (nt + c0)), off = static_cast<int>(in % (nt + c0)), t = max(0, off - c0);
+      int u = static_cast<int>(in / (nt + c0)), t = 0;
+      const int off = static_cast<int>(in % (nt + c0));
+      if (!p.whole)
+        t = max(0, off - c0);
+      else if (off != 0)
+        ++u;  // the next unit; behind the last, the next sequence's first
       const long long done = (from >> 32) * U + static_cast<long long>(u) * nt + t;  // tiles before it
+      while (u == U && b < B) {
+        ++b;
+        if (tiles_of(b) != 0) u = 0;
+      }
       if (e) {
         red[12] = done;
         red[13] = at - off + nt + c0;
@@ -306,6 +328,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   ft = static_cast<int>(red[10]);
   cnt = static_cast<int>(red[12] - red[11]);
   last_end = red[13];
+  if (cnt == 0) return;  // p.whole: no unit starts in the share
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == kPagedWarps) {
@@ -370,7 +393,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     int n = 0;
     for (; n < cnt; ++n) {
       const Tile next = fetch(n + 1);
-      if (!__all_sync(0xffffffffu, n < ST || mbar_wait(empty + st, ph, abort))) break;
+      if (!__all_sync(0xffffffffu, n < ST || paged_wait(empty + st, ph, abort))) break;
       const bool on = cur.page >= 0 && cur.page < p.c.num_pages;
       const uint32_t boxes = __ballot_sync(0xffffffffu, on);
       // boxes up to the end of the last group of 32 keys; those on no page are filled with zeros
@@ -484,7 +507,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   auto join = [&] {  // the computing warps meet; false: given up
     __syncwarp();
     if (lane == 0) mbar_arrive(joined);
-    const bool ok = mbar_wait(joined, jph, abort);
+    const bool ok = paged_wait(joined, jph, abort);
     jph ^= 1;
     return __all_sync(0xffffffffu, ok) != 0;
   };
@@ -514,7 +537,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 
   load_q(fb, fu * p.lanes + ulane);
   for (int n = 0; n < cnt; ++n) {
-    if (!__all_sync(0xffffffffu, mbar_wait(full + st, ph, abort))) return;
+    if (!__all_sync(0xffffffffu, paged_wait(full + st, ph, abort))) return;
     const PagedDesc& t = desc[st];
     const int key0 = t.key0, flags = t.flags, left = t.end - t.key0;
     const uint32_t boxes = t.boxes, all_boxes = 0xffffffffu >> (32 - (TK >> p.box_log));
@@ -843,7 +866,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     const bool whole = seg_starts_unit && (flags & kFlagUnitEnd);
     const int slot = 2 * cta + (seg_starts_unit ? 1 : 0);
     if (n + 1 < cnt) load_q(t.next_b, t.next_unit);  // the next unit's queries, on their way meanwhile
-    if (n == cnt - 1 && tid == 0) {
+    if (n == cnt - 1 && tid == 0 && !p.whole) {
       int4 s = make_int4(0, 0, 0, 0);
       if (seg_starts_unit && !(flags & kFlagUnitEnd))  // goes on in the next CTAs
         s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - group + 1, 0);
