@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   const int hg = warp / (RG * KW), rg = warp / KW % RG, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
   uint32_t qb[NB][QS][2];  // Q^T: row rq of each block, the k index in the order of the K fragments
   float acc[NB][DT][4];    // O^T: columns dcol(x, 0), dcol(x, 1) of V for rows 2 qd, 2 qd + 1
-  float m[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2];
+  float mneg[NB][2], lim[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2], vtop = 0.f, vlow = 0.f;
   int rlo[NB][2], rhi[NB][2];  // padded positions that the thread's rows may see
   int free_lo = 0, free_hi = 0;  // those that every row of the unit may see
   bool seg_starts_unit = false, fresh = true;  // fresh: the next tile begins a segment
@@ -570,10 +570,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          m[nb][c] = -INFINITY;
+          mneg[nb][c] = 0.f;
+          lim[nb][c] = -INFINITY;
           l[nb][c] = 0.f;
-          vref[nb][c] = __uint_as_float(1u << 23);   // 2^-126
-          vinv[nb][c] = __uint_as_float(253u << 23);
+          vref[nb][c] = 0x1p-126f;
+          vinv[nb][c] = 0.f;
           rowf[nb][c] = kQuant ? __shfl_sync(0xffffffffu, back, (2 * qd + c) * 4) : back;
           const int r = row0 + nb * 8 + 2 * qd + c;
           const int i = p.Nq == 1 ? 0 : r % p.Nq, pos = L - p.Nq + i;
@@ -587,6 +588,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
         for (int x = 0; x < DT; ++x) acc[nb][x][0] = acc[nb][x][1] = acc[nb][x][2] = acc[nb][x][3] = 0.f;
       }
+      vtop = vlow = 0.f;
       free_lo = p.window < 0 ? 0 : paged_pad(p, max(0, L - 1 - p.window));
       free_hi = 0;
       if (L >= p.Nq)
@@ -642,10 +644,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                sc[k][nb][2 * h + c] *= rowf[nb][c];
+              for (int c = 0; c < 2; ++c)
                 if (kQuant) sc[k][nb][2 * h + c] *= ks;
-              }
           }
         uint32_t allowed = 0xffffffffu;  // bit 4 (k NB + nb) + e
         if (edge) {
@@ -678,54 +678,77 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         // ---- running maximum: moved only when it grows by more than 8 (weights
         // stay below 2^8).  Quantised: weights reach the second product as f16
         // multiples of the largest value scale so far (vref, a power of two above
-        // it); a row's accumulator counts in units of its vref.
+        // it); a row's accumulator counts in units of its vref.  vtop and vlow
+        // bound the scales that leave all of a thread's rows as they are.
+        float arg[KS][NB][4];  // exponents: score - maximum, or the score itself before a row's first key (lim = -infinity)
         bool grow = false;
-        float mx[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            mx[nb][c] = fmaxf(sc[0][nb][c], sc[0][nb][2 + c]);
-            if (KS == 2) mx[nb][c] = fmaxf(mx[nb][c], fmaxf(sc[KS - 1][nb][c], sc[KS - 1][nb][2 + c]));
-            grow |= mx[nb][c] > m[nb][c] + 8.f;
-            if (kQuant)
+            float mx = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) grow |= fabsf(vs[k][h]) >= vref[nb][c] && on(k, nb, 2 * h + c);
+              for (int e = c; e < 4; e += 2) {
+                arg[k][nb][e] = fmaf(sc[k][nb][e], rowf[nb][c], mneg[nb][c]);
+                mx = fmaxf(mx, arg[k][nb][e]);
+              }
+            grow |= mx > lim[nb][c];
           }
+        if (kQuant)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) grow |= fmaxf(fabsf(vs[k][0]), fabsf(vs[k][1])) >= vtop;
         if (__any_sync(0xffffffffu, grow)) {
+          vtop = 0x1p127f;
+          vlow = 0.f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+              float mx = -INFINITY;
               uint32_t ve = 0;
-              if (kQuant)
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
+              for (int k = 0; k < KS; ++k)
 #pragma unroll
-                  for (int h = 0; h < 2; ++h)
-                    if (on(k, nb, 2 * h + c)) ve = max(ve, (__float_as_uint(vs[k][h]) >> 23) & 0xffu);
+                for (int h = 0; h < 2; ++h) {
+                  mx = fmaxf(mx, sc[k][nb][2 * h + c] * rowf[nb][c]);
+                  if (kQuant && on(k, nb, 2 * h + c)) ve = max(ve, (__float_as_uint(vs[k][h]) >> 23) & 0xffu);
+                }
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) {
-                mx[nb][c] = fmaxf(mx[nb][c], __shfl_xor_sync(0xffffffffu, mx[nb][c], o));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 if (kQuant) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, o));
               }
-              const float mn = mx[nb][c] > m[nb][c] + 8.f ? mx[nb][c] : m[nb][c];
-              float f = m[nb][c] == mn ? 1.f : exp2_fast(m[nb][c] - mn);
-              m[nb][c] = mn;
+              const float mo = lim[nb][c] == -INFINITY ? -INFINITY : -mneg[nb][c];
+              const float mn = mx > mo + 8.f ? mx : mo;
+              float f = mo == mn ? 1.f : exp2_fast(mo - mn);
+              if (mn != -INFINITY) {
+                mneg[nb][c] = -mn;
+                lim[nb][c] = 8.f;
+              }
               l[nb][c] *= f;
               if (kQuant) {
-                const float vn = fmaxf(vref[nb][c], __uint_as_float(min(ve + 1u, 253u) << 23));
-                vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
-                f *= vref[nb][c] * vinv[nb][c];
-                vref[nb][c] = vn;
+                if (ve != 0) {
+                  const float vn = fmaxf(vref[nb][c], __uint_as_float(min(ve + 1u, 253u) << 23));
+                  vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
+                  f *= vref[nb][c] * vinv[nb][c];
+                  vref[nb][c] = vn;
+                }
+                if (vref[nb][c] > 0x1p-126f) {
+                  vtop = fminf(vtop, vref[nb][c]);
+                  vlow = fmaxf(vlow, vref[nb][c] * 0x1p-12f);
+                }
               }
 #pragma unroll
               for (int x = 0; x < DT; ++x) {
                 acc[nb][x][c] *= f;
                 acc[nb][x][2 + c] *= f;
               }
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = c; e < 4; e += 2) arg[k][nb][e] = fmaf(sc[k][nb][e], rowf[nb][c], mneg[nb][c]);
             }
         }
         // The weights are rounded to 16 bits for the second product: bf16 (half a
@@ -737,19 +760,17 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           slow[k] = false;
+          if (kQuant)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) slow[k] |= fabsf(vs[k][h]) < vlow && fabsf(vs[k][h]) > 0x1p-90f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float mu = m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1];
-              const float w = exp2_fast(sc[k][nb][e] - mu);
+              const float w = exp2_fast(arg[k][nb][e]);
               l[nb][e & 1] += w;
               sc[k][nb][e] = w;
-              if (kQuant) {
-                const float u = vs[k][e >> 1] * vinv[nb][e & 1];
-                slow[k] |= on(k, nb, e) && fabsf(u) < 0x1p-12f && fabsf(vs[k][e >> 1]) > 0x1p-90f;
-                sc[k][nb][e] = on(k, nb, e) ? w * u : 0.f;
-              }
+              if (kQuant) sc[k][nb][e] = on(k, nb, e) ? w * (vs[k][e >> 1] * vinv[nb][e & 1]) : 0.f;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -872,12 +893,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - group + 1, 0);
       p.split[cta] = s;
     }
+    float m[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c) {
+        m[nb][c] = lim[nb][c] == -INFINITY ? -INFINITY : -mneg[nb][c];
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], o);
+      }
     if constexpr (KW == 1) {  // the warp's rows are its own
       release();
 #pragma unroll
