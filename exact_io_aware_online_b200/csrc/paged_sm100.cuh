@@ -197,6 +197,11 @@ __device__ __forceinline__ int paged_slot(const PagedParams& p, int padded) {  /
   return padded - pad_page_of(p, padded) * p.pad_page;
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where they do, a fraction of the 64-bit division's instructions.
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 struct PagedDesc {  // a tile, as the loading warp describes it to the others
   int b, unit, key0, end;
   int flags, L;
@@ -230,6 +235,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   const int cta = blockIdx.x, B = p.c.B;
   const int group = cta / p.lanes, ulane = cta - group * p.lanes, groups = gridDim.x / p.lanes;
   const int U = p.c.Hkv / HG * p.nblk / p.lanes;  // units of a sequence in a lane: ulane + lanes * (0 .. U - 1)
+  int stall = 0;
+  if (warp == kPagedWarps) {  // what the loading warp needs from far away, while the share is found
+    stall = *static_cast<volatile int*>(&g_debug_stall);
+    prefetch_tmap(&map_k);
+    prefetch_tmap(&map_v);
+  }
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(full + i, kQuant ? 33 : 1);
@@ -264,8 +275,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   auto cost = [&](long long x) { return ((x >> 32) + (x & 0xffffffffLL) * c0) * U; };
   const long long W = cost(sum);
   // groups with a share: c0 + 1 or more, so that each holds a tile
-  const long long G = min(static_cast<long long>(groups), W / (c0 + 1));
-  const long long s0 = group < G ? group * W / G : 0, s1 = group < G ? (group + 1) * W / G : 0;
+  const long long G = min(static_cast<long long>(groups), c0 ? W >> 1 : W);
+  const long long s0 = group < G ? paged_div(group * W, G) : 0, s1 = group < G ? paged_div((group + 1) * W, G) : 0;
 
   // rows of sequences without keys
   for (int b = cta; b < B; b += gridDim.x) {
@@ -299,8 +310,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         continue;
       }
       const long long in = at - cost(from);
-      int u = static_cast<int>(in / (nt + c0)), t = 0;
-      const int off = static_cast<int>(in % (nt + c0));
+      int u = static_cast<int>(paged_div(in, nt + c0)), t = 0;
+      const int off = static_cast<int>(in - static_cast<long long>(u) * (nt + c0));
       if (!p.whole)
         t = max(0, off - c0);
       else if (off != 0)
@@ -333,9 +344,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 
   if (warp == kPagedWarps) {
     // ---- the loading warp
-    prefetch_tmap(&map_k);
-    prefetch_tmap(&map_v);
-    if (*static_cast<volatile int*>(&g_debug_stall)) return;
+    if (stall) return;
     const int box = 1 << p.box_log;
     int fL = cache_length(p.c, fb), fLnext = fb + 1 < B ? cache_length(p.c, fb + 1) : 0;
     int2 span = paged_span(p, fL);
@@ -890,7 +899,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     if (n == cnt - 1 && tid == 0 && !p.whole) {
       int4 s = make_int4(0, 0, 0, 0);
       if (seg_starts_unit && !(flags & kFlagUnitEnd))  // goes on in the next CTAs
-        s = make_int4(b, unit, static_cast<int>((last_end * G - 1) / W) - group + 1, 0);
+        s = make_int4(b, unit, static_cast<int>(paged_div(last_end * G - 1, W)) - group + 1, 0);
       p.split[cta] = s;
     }
     float m[NB][2];
