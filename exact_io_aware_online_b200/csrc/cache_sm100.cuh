@@ -60,6 +60,12 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t x) {
   return __half22float2(__half2(h));
 }
 
+// Every kernel here is launched to begin while the one before it ends, and
+// waits for that one's results (and for its reads of what is written) with this.
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel may begin (and wait) once every block has said this.
+__device__ __forceinline__ void let_successor_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- moving tokens
 struct MoveParams {
   CacheParams c;
@@ -124,6 +130,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) cache_move_kernel(const MoveP
     return (isv[u] ? p.v + 2 * (token[u] * p.v_row + head[u] * p.v_head) : p.k + 2 * (token[u] * p.k_row + head[u] * p.k_head)) +
            q * 16;
   };
+  wait_for_predecessor();
   if (kWrite) {
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
@@ -133,6 +140,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) cache_move_kernel(const MoveP
     }
   }
 
+  let_successor_begin();
   // ---- where the rows live: the sequence of the warp's first token, from which each lane goes on to its own
   const int t0 = token_of(first);
   const int b0 = first_sequence(p.cu, p.c.B, t0, lane);

@@ -35,10 +35,9 @@ fa_status check_stream(void* stream) {
   return sdev == cur ? FA_OK : FA_ERR_INVALID_ARG;
 }
 
-// dependent: the kernel starts early and waits (griddepcontrol.wait) for the one before it.
+// The kernel may begin while the one before it in the stream ends; it waits for that one itself.
 template <typename... KArgs, typename... Args>
-fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool dependent,
-                 Args&&... args) {
+fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -48,7 +47,7 @@ fa_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, c
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -158,10 +157,10 @@ fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_st
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = cache->dtype == FA_CACHE_E4M3;
   if (d == 64)
-    return quant ? launch(fa::cache_move_kernel<64, true, kWrite>, grid, block, 0, st, false, p)
-                 : launch(fa::cache_move_kernel<64, false, kWrite>, grid, block, 0, st, false, p);
-  return quant ? launch(fa::cache_move_kernel<128, true, kWrite>, grid, block, 0, st, false, p)
-               : launch(fa::cache_move_kernel<128, false, kWrite>, grid, block, 0, st, false, p);
+    return quant ? launch(fa::cache_move_kernel<64, true, kWrite>, grid, block, 0, st, p)
+                 : launch(fa::cache_move_kernel<64, false, kWrite>, grid, block, 0, st, p);
+  return quant ? launch(fa::cache_move_kernel<128, true, kWrite>, grid, block, 0, st, p)
+               : launch(fa::cache_move_kernel<128, false, kWrite>, grid, block, 0, st, p);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -264,14 +263,14 @@ fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStrea
   }
   p.whole = (keys + C::kTile - 1) / C::kTile <= fa::kPagedWhole;
   const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles * (units / p.lanes)));
-  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, false, mk, mv, p);
+  const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, mk, mv, p);
   if (s != FA_OK || p.whole) return s;
   // four warps a row where there are few rows (a wave of warps, and few blocks without work)
   const bool few = HG * p.prow <= 8 && static_cast<long long>(p.c.B) * p.H * p.Nq <= 148 * 16;
   const int rows = fa::kPagedCombineWarps / (few ? 4 : 1);
   const dim3 grid(ctas, (HG * p.prow + rows - 1) / rows), block(32 * fa::kPagedCombineWarps);
-  return few ? launch(fa::paged_combine_kernel<D, kQuant, 4>, grid, block, 0, st, true, p, C::kRows, HG)
-             : launch(fa::paged_combine_kernel<D, kQuant, 1>, grid, block, 0, st, true, p, C::kRows, HG);
+  return few ? launch(fa::paged_combine_kernel<D, kQuant, 4>, grid, block, 0, st, p, C::kRows, HG)
+             : launch(fa::paged_combine_kernel<D, kQuant, 1>, grid, block, 0, st, p, C::kRows, HG);
 }
 
 template <int D, bool kQuant>

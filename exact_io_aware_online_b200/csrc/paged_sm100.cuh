@@ -251,6 +251,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     fence_mbar_init();
   }
 
+  wait_for_predecessor();
+
   // ---- this group's share [s0, s1) of the list, in which a unit counts its tiles and c0
   auto tiles_of = [&](int b) { return b < B ? paged_tiles<TK>(p, cache_length(p.c, b)) : 0; };
   auto packed = [](int nt) { return (static_cast<long long>(nt) << 32) + (nt != 0); };  // tiles, sequences with keys
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   cnt = static_cast<int>(red[12] - red[11]);
   last_end = red[13];
   if (cnt == 0) return;  // p.whole: no unit starts in the share
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_successor_begin();
 
   if (warp == kPagedWarps) {
     // ---- the loading warp
@@ -1057,7 +1059,7 @@ __global__ void __launch_bounds__(32 * kPagedCombineWarps)
   constexpr int E = D / 32, kRows = kPagedCombineWarps / CW;
   __shared__ float4 stat[kRows][CW];
   __shared__ float part[CW > 1 ? kRows : 1][CW][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_predecessor();
   const int4 s = p.split[blockIdx.x];
   const int parts = s.z;
   if (parts == 0) return;
