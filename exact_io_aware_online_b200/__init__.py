@@ -684,7 +684,7 @@ def cache_write(k, v, k_pages, v_pages, page_table, cu_seqlens, seqlens, k_scale
     float8_e4m3fn; page_table [B,pages of a sequence], cu_seqlens and seqlens
     int32, all on one CUDA device."""
     c, device, B, Hkv, d = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
-    T = k.shape[0]
+    T = len(k)
     st = _move_args(B, Hkv, d, k, v, cu_seqlens, T, device)
     if T == 0:
         return

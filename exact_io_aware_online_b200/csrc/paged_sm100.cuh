@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   }
 
   wait_for_predecessor();
+  // nothing to join, until this CTA has come to its end: one that gives up leaves it at that
+  if (tid == 0 && !p.whole) p.split[cta] = make_int4(0, 0, 0, 0);
 
   // ---- this group's share [s0, s1) of the list, in which a unit counts its tiles and c0
   auto tiles_of = [&](int b) { return b < B ? paged_tiles<TK>(p, cache_length(p.c, b)) : 0; };
@@ -291,10 +293,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
       p.lse[static_cast<long long>(b) * p.H * p.Nq + r] = -INFINITY;
     }
   }
-  if (group >= G) {
-    if (tid == 0 && !p.whole) p.split[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
+  if (group >= G) return;
 
   // ---- the front cursor: sequence, unit and tile of s0; the tiles up to s1
   int fb, fu, ft, cnt;
@@ -898,12 +897,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
     const bool whole = seg_starts_unit && (flags & kFlagUnitEnd);
     const int slot = 2 * cta + (seg_starts_unit ? 1 : 0);
     if (n + 1 < cnt) load_q(t.next_b, t.next_unit);  // the next unit's queries, on their way meanwhile
-    if (n == cnt - 1 && tid == 0 && !p.whole) {
-      int4 s = make_int4(0, 0, 0, 0);
-      if (seg_starts_unit && !(flags & kFlagUnitEnd))  // goes on in the next CTAs
-        s = make_int4(b, unit, static_cast<int>(paged_div(last_end * G - 1, W)) - group + 1, 0);
-      p.split[cta] = s;
-    }
+    if (n == cnt - 1 && tid == 0 && seg_starts_unit && !(flags & kFlagUnitEnd))  // the unit goes on in the next CTAs
+      p.split[cta] = make_int4(b, unit, static_cast<int>(paged_div(last_end * G - 1, W)) - group + 1, 0);
     float m[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
