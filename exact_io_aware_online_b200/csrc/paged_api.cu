@@ -139,6 +139,8 @@ fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_st
   fa::Strides sk, sv;
   if ((s = check_strides(strides ? strides[0] : packed, 1, Hkv, T, d, 2, 16, !kWrite, &sk)) != FA_OK) return s;
   if ((s = check_strides(strides ? strides[1] : packed, 1, Hkv, T, d, 2, 16, !kWrite, &sv)) != FA_OK) return s;
+  const long long rows = 2LL * Hkv * T;
+  if (rows > (1LL << 31) - fa::kMoveWarps * fa::kMoveRows) return FA_ERR_UNSUPPORTED;  // counted in 32 bits
   if ((s = check_stream(stream)) != FA_OK) return s;
   p.k = static_cast<uint8_t*>(k);
   p.v = static_cast<uint8_t*>(v);
@@ -148,9 +150,6 @@ fa_status move_tokens(const fa_paged_cache* cache, void* k, void* v, const fa_st
   p.v_head = sv.h;
   p.cu = cu;
   p.T = T;
-  const long long rows = 2LL * Hkv * T;
-  if (rows > (1LL << 31) - fa::kMoveWarps * fa::kMoveRows) return FA_ERR_UNSUPPORTED;  // counted in 32 bits
-  if (Hkv > (1 << 29)) return FA_ERR_UNSUPPORTED;
   magic(2 * Hkv, &p.row_mul, &p.row_shift);
   const long long blocks = (rows + fa::kMoveWarps * fa::kMoveRows - 1) / (fa::kMoveWarps * fa::kMoveRows);
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * fa::kMoveWarps);
@@ -253,8 +252,6 @@ fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStrea
   // no more groups than the lengths could give tiles
   const long long cap = static_cast<long long>(p.c.max_pages) * p.pad_page;
   const double tiles = static_cast<double>((cap + C::kTile - 1) / C::kTile) * p.c.B;  // of one unit of each sequence
-  // tiles are counted in 32 bits: those of a CTA, and of all sequences
-  if (tiles > 2e9 || tiles * units / most > 1e9) return FA_ERR_UNSUPPORTED;
   // tiles of a unit at most: of the table's tokens, or of a window's and the pages and boxes it cuts
   long long keys = cap;
   if (p.window >= 0) {
@@ -343,6 +340,15 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   if ((s = check_strides(strides ? strides[1] : dense, B, H, Nq, d, 2, 16, true, &p.so)) != FA_OK) return s;
   if (!workspace || ws_bytes < fa_fwd_paged_workspace_size(B, H, Hkv, Nq, d)) return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_MISALIGNED;
+  p.pad_page = (cache->page_size + 7) & ~7;
+  p.R = H / Hkv * Nq;
+  const int block = paged_rows(p.R);
+  p.nblk = (p.R + block - 1) / block;
+  // positions are 32-bit with pages rounded up too, and so are the counts of tiles (of 16 keys or more): those of all
+  // sequences and of a CTA
+  const long long cap = static_cast<long long>(cache->max_pages) * p.pad_page;
+  const double tiles = static_cast<double>(cap) / 16 * B;
+  if (cap > (1LL << 30) || tiles > 2e9 || tiles / 296 * Hkv * p.nblk > 2e9) return FA_ERR_UNSUPPORTED;
   if ((s = check_stream(stream)) != FA_OK) return s;
   p.q = static_cast<const uint8_t*>(q);
   p.o = static_cast<uint8_t*>(o);
@@ -354,9 +360,6 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.causal = causal ? 1 : 0;
   p.window = window < (1 << 30) ? window : -1;  // positions stay below 2^30
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  p.R = p.g * Nq;
-  const int block = paged_rows(p.R);
-  p.nblk = (p.R + block - 1) / block;
   p.prow = std::min(p.R, block);
   const bool quant = cache->dtype == FA_CACHE_E4M3;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -364,9 +367,7 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.split = reinterpret_cast<int4*>(ws);
   p.part_m = reinterpret_cast<float4*>(ws + at.part_m);
   p.part_o = reinterpret_cast<float*>(ws + at.part_o);
-  p.pad_page = (cache->page_size + 7) & ~7;
   magic(p.pad_page, &p.pad_mul, &p.pad_shift);
-  if (static_cast<long long>(cache->max_pages) * p.pad_page > (1LL << 30)) return FA_ERR_UNSUPPORTED;  // padded positions are 32-bit too
   if (d == 64) return quant ? launch_paged_rows<64, true>(cache, p, st) : launch_paged_rows<64, false>(cache, p, st);
   return quant ? launch_paged_rows<128, true>(cache, p, st) : launch_paged_rows<128, false>(cache, p, st);
 }

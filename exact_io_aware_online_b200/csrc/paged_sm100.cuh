@@ -8,34 +8,46 @@
 // (base 2, rescaled only when the maximum grows by more than 2^8).
 //
 // What bounds it: every key and value crosses HBM once and meets the g * Nq
-// rows that share its kv head, 2 * rows flops a byte (bf16): below 64 rows far
+// rows that share its kv head, 2 * rows flops a byte (bf16): up to 16 rows far
 // under what mma.sync delivers, so the kernel is laid out for bytes in flight
 // and few instructions, not for the tensor pipe.  Both products are formed
 // transposed, S^T = K Q^T and O^T = V^T P^T, so that the 16 of m16n8k16 is
 // filled by keys and by columns of V and only the rows are padded, to 8.
+// Quantised pages cost two conversions for four codes besides, each a quarter
+// of a warp instruction's rate: they and the rows' exponentials bound the
+// kernel from 16 rows on.
 //
 // Work: the keys that some row of a unit (sequence, 1 to 4 kv heads, block of
-// rows) may see are cut into tiles of 16 to 128, about 32 KB.  The CTAs form groups of `lanes`, a lane
-// for each unit of a sequence (or every lanes-th), so that a group reads the
-// same tokens' heads at the same time: heads inside tokens are then whole DRAM
-// rows, the 32-byte sectors of the scales are read from DRAM once, and blocks
-// of rows share their keys in L2.  The tiles of all sequences form one list, and
-// group c of G takes its c-th even share, whatever the lengths (beginning a
-// unit counts as much as a tile).  In each CTA one warp walks the share, looks
-// pages up and keeps a ring of tiles loading (TMA boxes of 8 to 32 tokens, each
-// inside a page, over the unit's kv heads; scales by cp.async), on from one unit
-// into the next; four warps compute, where the kv heads allow it each its own
-// head or rows, so that they never meet; otherwise they share a tile's keys and
-// join their states at a unit's end.  A unit that lies in one share is finished
-// by its CTA; one that several share leaves a partial (m, l,
+// rows) may see are cut into tiles of 16 to 128, about 32 KB.  The CTAs form
+// groups of `lanes`, a lane for each unit of a sequence (or every lanes-th), so
+// that a group reads the same tokens' heads at the same time: heads inside
+// tokens are then whole DRAM rows, the 32-byte sectors of the scales are read
+// from DRAM once, and blocks of rows share their keys in L2.  The tiles of all
+// sequences form one list, and group c of G takes its c-th even share, whatever
+// the lengths (beginning a unit counts as much as a tile: with tiles alone 64
+// ragged sequences took 168 us against 141 us).  In each CTA one warp walks the
+// share, looks pages up and keeps a ring of tiles loading (TMA boxes of 8 to 32
+// tokens, each inside a page, over the unit's kv heads; scales by cp.async), on
+// from one unit into the next; four warps compute, where the kv heads allow it
+// each its own head or rows, so that they never meet; otherwise they share a
+// tile's keys and join their states at a unit's end.  A unit that lies in one
+// share is finished by its CTA; one that several share leaves a partial (m, l,
 // accumulator) per CTA -- at most two per CTA, so the workspace does not grow
-// with the batch -- for paged_combine_kernel.  Where no unit can have more than
-// kPagedWhole tiles, none is shared: its group is the one its first tile falls
-// to, and there is nothing to combine.
+// with the batch -- for paged_combine_kernel (joining by the last CTA to arrive
+// instead was slower wherever units are shared: one token over 32000 266 us
+// against 37 us, 128 quantised sequences of 512 84 us against 51 us).  Where no
+// unit can have more than kPagedWhole tiles, none is shared: its group is the
+// one its first tile falls to, and there is nothing to combine.
 //
 // Positions inside the kernel are padded: a page counts as page_size rounded up
 // to 8 tokens, so that a box never spans two pages; the slots that do not exist
 // are zero-filled by the TMA and masked.
+//
+// Measured (one call among others, 32 query heads on 8 kv heads, d = 128, of the
+// copy rate of 6561 GB/s): one token over 8 x 32768 tokens, bf16, 167 us (98%); 64
+// ragged sequences, bf16, 119 us (93%); 128 ragged sequences, e4m3, 64 query heads,
+// 101 us (80%); four tokens each of 16 sequences, e4m3, 50 us (49%); 256 sequences, 16 heads,
+// d = 64, window 255, 32 us (58%).
 #pragma once
 
 #include <type_traits>
@@ -49,7 +61,7 @@ constexpr int kPagedWarps = 4;      // that compute; one more loads
 constexpr int kPagedThreads = 32 * (kPagedWarps + 1);
 constexpr int kPagedMaxCtas = 444;  // three on each of 148 SMs
 constexpr int kPagedCombineWarps = 8;
-constexpr int kPagedWhole = 4;
+constexpr int kPagedWhole = 4;      // tiles: one CTA takes them in about the time of the second kernel
 
 struct PagedParams {
   CacheParams c;
@@ -82,7 +94,9 @@ struct PagedCfg {
   static constexpr int kRows = 8 * NB * RG;
   static constexpr int KW = kPagedWarps / (HG * RG);
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
-  static constexpr int kTile = (kRowBytes == 256 || (kQuant && KW == 4 && D == 128) ? 64 : 128) / HG;  // keys
+  // keys: 32 KB of K and V, which two stages of three CTAs have room for; half of it where four warps share the keys
+  // of a quantised tile (128 ragged sequences 109 us against 121 us: more, smaller steps of the ring)
+  static constexpr int kTile = (kRowBytes == 256 || (kQuant && KW == 4 && D == 128) ? 64 : 128) / HG;
   static constexpr int kPart = kRowBytes == 256 ? 128 : kRowBytes;  // bytes of a row in a TMA box (its swizzle's width)
   static constexpr int kTileBytes = HG * kTile * kRowBytes;
   static constexpr int kScaleBytes = kQuant ? HG * kTile * 4 : 0;
@@ -220,7 +234,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   constexpr int DT = D / 16;                  // row tiles of O^T = V^T P^T
   constexpr int QS = D / 16;                  // k-steps of S^T = K Q^T
   constexpr int ST = C::kStages, RB = C::kRowBytes, PB = C::kPart, TK = C::kTile;
-  constexpr int KS = TK / KW >= 32 ? 2 : 1;   // groups of 16 keys that a warp takes together
+  // groups of 16 keys that a warp takes together: two, but where their registers spill (quantised, 16 rows a warp:
+  // 115 us with two, 112 us with one, at 64 rows on 16384 tokens of 8 sequences)
+  constexpr int KS = TK / KW >= 32 && !(kQuant && NB == 2) ? 2 : 1;
   constexpr int ES = kQuant ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   float4* stat = reinterpret_cast<float4*>(smem + ST * C::kStageBytes);     // [warps][8 * NB rows]: m, l, unit
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 
   // ---- the front cursor: sequence, unit and tile of s0; the tiles up to s1
   int fb, fu, ft, cnt;
-  long long last_end;  // where the unit that s1 lies in ends
+  long long last_end;  // where the unit that s1 lies in ends, on the list
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const long long at = e ? s1 : s0;

@@ -295,7 +295,8 @@ typedef struct {
  * of fa_fwd_strided (and so must the pages' for fa_cache_write).
  * T = 0 enqueues nothing.  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
  * Errors: FA_ERR_INVALID_ARG for null pointers, sizes < 1, T < 0 or bad
- * strides; FA_ERR_UNSUPPORTED for d not in {64, 128}; FA_ERR_MISALIGNED.
+ * strides; FA_ERR_UNSUPPORTED for d not in {64, 128}, for page_size * max_pages
+ * above 2^30, and for 2 * Hkv * T near 2^31 and above; FA_ERR_MISALIGNED.
  */
 fa_status fa_cache_write(const fa_paged_cache* cache, const void* k, const void* v, const fa_strides* strides,
                          const int* cu_seqlens_dev, int T, fa_dtype dtype, void* stream);
@@ -315,13 +316,21 @@ fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_
  * parts of pages hold has no effect.  Every key and value that some row may see
  * is read once for the H / Hkv query heads that share it, as long as their
  * (H / Hkv) * Nq rows are at most 64 (once per 64 rows otherwise).
+ * Any page_size goes; multiples of 16 load best (others are taken as the next
+ * multiple of 8 tokens long: page_size rounded up so, times max_pages, is at
+ * most 2^30, FA_ERR_UNSUPPORTED otherwise).
  * The key ranges of all sequences are dealt out evenly over the SMs, and
  * sequences that several of them share are merged from partial online-softmax
  * states (fa_fwd_splitkv) in the workspace: at least
  * fa_fwd_paged_workspace_size() bytes of device memory, 16-byte aligned,
- * contents irrelevant on entry, not shared by calls that may overlap.
+ * contents irrelevant on entry, not shared by calls that may overlap (graphs
+ * that may be replayed at the same time among them).
  * Deterministic; a sequence's last bits depend on the other lengths of the
- * batch.  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
+ * batch.  Arithmetic: scores, maxima, sums and accumulators in fp32; the
+ * weights enter the second product as bf16 (bf16 pages) or, times the value's
+ * scale, as f16 (E4M3 pages).  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
+ * Other errors as fa_fwd; FA_ERR_UNSUPPORTED also where the table could hold
+ * more tiles than 32 bits count.
  */
 size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d);
 fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,
@@ -413,7 +422,7 @@ void fa_set_timing_events(void* start, void* stop);
  *   copies and tensor-core operations in flight, frees its tensor memory and
  *   returns; the outputs of that call are then undefined.
  * fa_debug_set_stall: while nonzero, the sm_100a kernels never issue their
- *   first tile load (K/V in the backward, Q in the forward), so every CTA's
+ *   first tile load (K/V in the backward and in fa_fwd_paged, Q in the forward), so every CTA's
  *   waits for it run out and the call reports FA_ERR_TIMEOUT through
  *   fa_last_device_status(); 0 restores normal operation.  The fp32 path has
  *   no waits and ignores it.

@@ -161,3 +161,16 @@ def test_host_tensors_never_reach_a_kernel():
     q = torch.zeros((3, 4, 1, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         fa.fwd_paged(q, **host())
+
+
+def test_positions_are_counted_with_pages_rounded_up(L):
+    wide = dict(max_pages=1 << 28, table_stride=1 << 28)
+    assert attend(L, cache(page_size=1, **wide)) == UNSUPPORTED                 # 2^31 places of pages of 8
+    many = dict(page_size=1 << 20, max_pages=1 << 10, table_stride=1 << 10, B=1 << 20)
+    many["pages"] = fa._Strides(1 << 28, 1 << 27, 64)
+    assert attend(L, cache(**many), ws_bytes=1 << 40) == UNSUPPORTED            # 2^50 tokens in all
+
+
+def test_more_rows_than_the_move_counts(L):
+    for fn in ("fa_cache_write", "fa_cache_read"):
+        assert write(L, cache(Hkv=2), T=(1 << 29), fn=fn) == UNSUPPORTED
