@@ -258,7 +258,12 @@ fa_status launch_paged(const fa_paged_cache* cache, fa::PagedParams p, cudaStrea
     const long long seen = static_cast<long long>(p.window) + p.Nq;
     keys = std::min(cap, (seen + 2 * p.c.page_size - 2) / p.c.page_size * p.pad_page);
   }
-  p.whole = (keys + C::kTile - 1) / C::kTile <= fa::kPagedWhole;
+  // units of up to kPagedWhole tiles are never shared, and of up to twice as many where one for each group keeps a
+  // quarter of the groups or more at work (device time, shared against whole: 32 x 500 tokens in bf16 24.0 and 18.9 us,
+  // 100 x 250 at d = 64 27.8 and 22.0 us; but one sequence of 500 10.3 and 14.8 us, 128 x 500 51.8 and 53.9 us)
+  const long long most_tiles = (keys + C::kTile - 1) / C::kTile, in_lane = static_cast<long long>(p.c.B) * (units / p.lanes),
+                  groups = most / p.lanes;
+  p.whole = most_tiles <= fa::kPagedWhole || (most_tiles <= 2 * fa::kPagedWhole && 4 * in_lane >= groups && in_lane <= groups);
   const int ctas = p.lanes * static_cast<int>(std::min<double>(most / p.lanes, tiles * (units / p.lanes)));
   const fa_status s = launch(kernel, dim3(ctas), dim3(fa::kPagedThreads), C::kSmemBytes, st, mk, mv, p);
   if (s != FA_OK || p.whole) return s;

@@ -36,8 +36,8 @@
 // with the batch -- for paged_combine_kernel (joining by the last CTA to arrive
 // instead was slower wherever units are shared: one token over 32000 266 us
 // against 37 us, 128 quantised sequences of 512 84 us against 51 us).  Where no
-// unit can have more than kPagedWhole tiles, none is shared: its group is the
-// one its first tile falls to, and there is nothing to combine.
+// unit can have more than a few tiles, none is shared: its group is the one its
+// first tile falls to, and there is nothing to combine.
 //
 // Positions inside the kernel are padded: a page counts as page_size rounded up
 // to 8 tokens, so that a box never spans two pages; the slots that do not exist

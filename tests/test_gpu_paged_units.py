@@ -257,3 +257,17 @@ def test_a_stalled_load_is_reported(Hkv, lens):
         fa.debug_set_wait_limit(0)
     assert fa.device_status() == 0
     compare(c, q)
+
+
+@pytest.mark.parametrize("kind,d,Hkv,B,longest", [("bf16", 128, 8, 20, 512), ("e4m3", 64, 4, 112, 256), ("bf16", 64, 1, 130, 700)])
+def test_units_of_several_tiles_that_are_not_shared(kind, d, Hkv, B, longest):
+    """Tables of at most eight tiles, and about as many sequences as groups of CTAs:
+    every unit stays with one group, some groups have none, empty sequences between."""
+    g = torch.Generator().manual_seed(321)
+    lens = torch.randint(0, longest + 1, (B,), generator=g).tolist()
+    lens[0], lens[1], lens[-1] = 0, longest, 0
+    c = Cache(lens, Hkv, d, 16, kind, "nhd", seed=322).fill_random(323)
+    compare(c, randn((B, Hkv, 1, d), 324))
+    empty = Cache([0] * B, Hkv, d, 16, kind, "nhd", seed=325, width=longest // 16)
+    o, lse = run(empty, randn((B, Hkv, 1, d), 326))
+    assert (o == 0).all() and (lse == -math.inf).all()
