@@ -33,9 +33,10 @@
 // tile's keys and join their states at a unit's end.  A unit that lies in one
 // share is finished by its CTA; one that several share leaves a partial (m, l,
 // accumulator) per CTA -- at most two per CTA, so the workspace does not grow
-// with the batch -- for paged_combine_kernel (joining by the last CTA to arrive
-// instead was slower wherever units are shared: one token over 32000 266 us
-// against 37 us, 128 quantised sequences of 512 84 us against 51 us).  Where no
+// with the batch -- for paged_combine_kernel (joining by the last warp to arrive
+// instead, four rows at a time, was slower wherever many units are shared, the
+// registers of both phases in one kernel: 128 ragged quantised sequences 111 us
+// against 97 us, four tokens of 16 sequences 71 us against 49 us).  Where no
 // unit can have more than a few tiles, none is shared: its group is the one its
 // first tile falls to, and there is nothing to combine.
 //

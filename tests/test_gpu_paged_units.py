@@ -271,3 +271,20 @@ def test_units_of_several_tiles_that_are_not_shared(kind, d, Hkv, B, longest):
     empty = Cache([0] * B, Hkv, d, 16, kind, "nhd", seed=325, width=longest // 16)
     o, lse = run(empty, randn((B, Hkv, 1, d), 326))
     assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_sequences_that_share_pages(kind):
+    """A common beginning kept once: several sequences name its pages, and the same page twice."""
+    c = Cache([96, 16, 130, 0], 2, 64, 16, kind, "nhd", seed=331).fill_random(332)
+    table = torch.full((4, 9), -1, dtype=torch.int32)
+    table[0, :6], table[2, :9] = c.table[0, :6], c.table[2, :9]
+    table[1, :4] = torch.tensor([table[0, 0], table[0, 1], table[0, 1], table[2, 0]])
+    table[3, :7] = torch.cat([table[0, :6], c.table[1, :1]])
+    c.table, c.lens = table, [96, 60, 130, 100]
+    c.seqlens = torch.tensor(c.lens, dtype=torch.int32)
+    compare(c, randn((4, 4, 2, 64), 333, 2.0))
+    (k, v, tab), scales = c.cuda()
+    cu = torch.tensor([0, 96, 156, 286, 386], dtype=torch.int32, device="cuda")
+    rk, _ = fa.cache_read(k, v, tab, cu, c.seqlens.cuda(), 386, **scales)
+    assert torch.equal(rk[286:382], rk[:96]) and torch.equal(rk[96:112], rk[:16]) and torch.equal(rk[112:128], rk[128:144])
