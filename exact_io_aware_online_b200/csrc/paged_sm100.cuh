@@ -985,19 +985,16 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
       }
     } else {
       // the KW warps of a row group join their states in tile n's stage
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (rq == 0) stat[(warp * NB + nb) * 8 + 2 * qd + c] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
-        }
       float* merge = reinterpret_cast<float*>(smem + st * C::kStageBytes);  // [warps][8 rows][kMergeStride]
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        if (!join()) return;  // tile n is read, the block before this one joined
+        // tile n is read; the block before this one is joined, and so is the segment before: its readers of stat,
+        // which no stage's barrier waits for, are behind it too
+        if (!join()) return;
         float* mine = merge + (warp * 8 + 2 * qd) * C::kMergeStride;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          if (rq == 0) stat[(warp * NB + nb) * 8 + 2 * qd + c] = make_float4(m[nb][c], l[nb][c], vref[nb][c], 0.f);
           if (row0 + (rg * NB + nb) * 8 + 2 * qd + c >= p.R) continue;
 #pragma unroll
           for (int x = 0; x < DT; ++x)
