@@ -62,6 +62,9 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t x) {
 
 // Every kernel here is launched to begin while the one before it ends, and
 // waits for that one's results (and for its reads of what is written) with this.
+// Loads behind it are plain ones: the read-only path (ld.global.nc) wants memory
+// that nobody writes from this kernel's first block on, and the kernel before,
+// which may still run then, writes tokens, pages and queries.
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next kernel may begin (and wait) once every block has said this.
 __device__ __forceinline__ void let_successor_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) cache_move_kernel(const MoveP
     for (int u = 0; u < kMoveUnroll; ++u) {
       const uint8_t* src = dense(u);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[u][i] = __ldg(reinterpret_cast<const uint4*>(src + i * 64));
+      for (int i = 0; i < N; ++i) x[u][i] = *reinterpret_cast<const uint4*>(src + i * 64);
     }
   }
 

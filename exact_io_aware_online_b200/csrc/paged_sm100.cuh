@@ -523,8 +523,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
       for (int s = 0; s < QS; ++s) {
         uint2 v = make_uint2(0, 0);
         if (r < p.R)
-          v = kQuant ? __ldg(reinterpret_cast<const uint2*>(qr + 8 * s + 2 * qd))
-                     : make_uint2(__ldg(qr + 8 * s + qd), __ldg(qr + 8 * s + 4 + qd));
+          v = kQuant ? *reinterpret_cast<const uint2*>(qr + 8 * s + 2 * qd) : make_uint2(qr[8 * s + qd], qr[8 * s + 4 + qd]);
         qb[nb][s][0] = v.x;
         qb[nb][s][1] = v.y;
       }
