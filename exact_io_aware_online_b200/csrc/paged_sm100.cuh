@@ -705,7 +705,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         // stay below 2^8).  Quantised: weights reach the second product as f16
         // multiples of the largest value scale so far (vref, a power of two above
         // it); a row's accumulator counts in units of its vref.  vtop and vlow
-        // bound the scales that leave all of a thread's rows as they are.
+        // bound the scales that leave all of a thread's rows as they are; a row
+        // that has seen scales of zero alone has no vref yet, and any other scale
+        // gives it one.
         float arg[KS][NB][4];  // exponents: score - maximum, or the score itself before a row's first key (lim = -infinity)
         bool grow = false;
 #pragma unroll
@@ -733,18 +735,18 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float mx = -INFINITY;
-              uint32_t ve = 0;
+              uint32_t vb = 0;  // the largest scale, as bits of its magnitude
 #pragma unroll
               for (int k = 0; k < KS; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   mx = fmaxf(mx, sc[k][nb][2 * h + c] * rowf[nb][c]);
-                  if (kQuant && on(k, nb, 2 * h + c)) ve = max(ve, (__float_as_uint(vs[k][h]) >> 23) & 0xffu);
+                  if (kQuant && on(k, nb, 2 * h + c)) vb = max(vb, __float_as_uint(vs[k][h]) & 0x7fffffffu);
                 }
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                if (kQuant) ve = max(ve, __shfl_xor_sync(0xffffffffu, ve, o));
+                if (kQuant) vb = max(vb, __shfl_xor_sync(0xffffffffu, vb, o));
               }
               const float mo = lim[nb][c] == -INFINITY ? -INFINITY : -mneg[nb][c];
               const float mn = mx > mo + 8.f ? mx : mo;
@@ -755,8 +757,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
               }
               l[nb][c] *= f;
               if (kQuant) {
-                if (ve != 0) {
-                  const float vn = fmaxf(vref[nb][c], __uint_as_float(min(ve + 1u, 253u) << 23));
+                if (vb != 0) {
+                  const float vn = fmaxf(vref[nb][c], __uint_as_float(min(max(vb >> 23, 1u) + 1u, 253u) << 23));
                   vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
                   f *= vref[nb][c] * vinv[nb][c];
                   vref[nb][c] = vn;
@@ -764,6 +766,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
                 if (vref[nb][c] > 0x1p-126f) {
                   vtop = fminf(vtop, vref[nb][c]);
                   vlow = fmaxf(vlow, vref[nb][c] * 0x1p-12f);
+                } else if (lim[nb][c] > 0.f) {
+                  vtop = 0x1p-149f;
                 }
               }
 #pragma unroll

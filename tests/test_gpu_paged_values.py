@@ -1,0 +1,53 @@
+"""Values, weights and scores of the paged calls at the ends of their ranges:
+value scales of zero, keys of most weight whose value is zero, weights far
+apart, factors that leave fp32's normal range, and the codes of extreme rows."""
+import math
+
+import pytest
+import torch
+
+import exact_io_aware_online_b200 as fa
+
+from paged_ref import Cache, attend, check, quantise
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from exact_io_aware_online_b200 import _build
+    _build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def randn(shape, seed, spread=1.0):
+    return (torch.randn(shape, generator=torch.Generator("cpu").manual_seed(seed)) * spread).to(torch.bfloat16)
+
+
+def compare(c, q, causal=True, window=-1, **kw):
+    args, scales = c.cuda()
+    o, lse = fa.fwd_paged(q.cuda(), *args, c.seqlens.cuda(), causal=causal, window=window, **scales, **kw)
+    torch.cuda.synchronize()
+    want_o, want_l, tol_o, tol_l = attend(c, q, causal, window, kw.get("scale"))
+    check("O", o, want_o, tol_o)
+    check("LSE", lse, want_l, tol_l)
+
+
+# sequences, kv heads, query heads a kv head, rows, head_dim: one and four kv heads a unit, 1 to 64 rows
+SHAPES = [(2, 1, 1, 1, 128), (16, 4, 1, 1, 128), (16, 4, 2, 1, 64), (2, 4, 1, 1, 64), (32, 2, 3, 4, 128), (96, 4, 1, 1, 128), (2, 1, 16, 4, 64), (3, 1, 5, 4, 128)]
+
+
+@pytest.mark.parametrize("B,Hkv,g,Nq,d", SHAPES)
+@pytest.mark.parametrize("zeros", [16, 32, 64, 130])
+def test_values_behind_scales_of_zero(B, Hkv, g, Nq, d, zeros):
+    """A sequence begins with tokens whose value scale is zero (a placeholder, or
+    another writer's rows of zeros) or subnormal; the tokens behind count in full."""
+    for small in (0.0, 2.0 ** -140):
+        for lens in ([170 + 9 * b for b in range(B - 1)] + [2500], [zeros + 1 + b % 60 for b in range(B)]):
+            c = Cache(lens, Hkv, d, 16, "e4m3", "nhd", seed=421).fill_random(422)
+            for b in range(B):
+                pid, slot = c.places(b, torch.arange(zeros))
+                c.t["v_scale"][pid, :, slot] = small
+            compare(c, randn((B, Hkv * g, Nq, d), 423, 2.0))
+            compare(c, randn((B, Hkv * g, Nq, d), 424, 2.0), window=160)
