@@ -333,7 +333,8 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
                        int H, int Nq, float scale, int causal, int window, void* workspace, size_t ws_bytes,
                        fa_dtype dtype, void* stream) {
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale) || window < -1) return FA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !std::isfinite(scale_log2) || window < -1) return FA_ERR_INVALID_ARG;
   fa::PagedParams p{};
   fa_status s = check_cache(cache, dtype, false, &p.c);
   if (s != FA_OK) return s;
@@ -361,7 +362,7 @@ fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, floa
   p.H = H;
   p.Nq = Nq;
   p.g = H / Hkv;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.causal = causal ? 1 : 0;
   p.window = window < (1 << 30) ? window : -1;  // positions stay below 2^30
   cudaStream_t st = static_cast<cudaStream_t>(stream);

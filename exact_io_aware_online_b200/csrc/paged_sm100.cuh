@@ -601,7 +601,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
           l[nb][c] = 0.f;
           vref[nb][c] = 0x1p-126f;
           vinv[nb][c] = 0.f;
-          rowf[nb][c] = kQuant ? __shfl_sync(0xffffffffu, back, (2 * qd + c) * 4) : back;
+          rowf[nb][c] = back;
+          // neither zero nor infinite: times a masked key's -infinity, or times a score of zero, those make NaN.  (A factor
+          // that underflows is that of scores of at most 2^-95 times the key's scale.)
+          if (kQuant) rowf[nb][c] = fminf(fmaxf(__shfl_sync(0xffffffffu, back, (2 * qd + c) * 4), 0x1p-149f), FLT_MAX);
           const int r = row0 + nb * 8 + 2 * qd + c;
           const int i = p.Nq == 1 ? 0 : r % p.Nq, pos = L - p.Nq + i;
           rlo[nb][c] = 0;

@@ -329,8 +329,9 @@ fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_
  * batch.  Arithmetic: scores, maxima, sums and accumulators in fp32; the
  * weights enter the second product as bf16 (bf16 pages) or, times the value's
  * scale, as f16 (E4M3 pages).  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
- * Other errors as fa_fwd; FA_ERR_UNSUPPORTED also where the table could hold
- * more tiles than 32 bits count.
+ * Other errors as fa_fwd; FA_ERR_INVALID_ARG also for a scale whose product
+ * with log2(e) overflows fp32, FA_ERR_UNSUPPORTED also where the table could
+ * hold more tiles than 32 bits count.
  */
 size_t fa_fwd_paged_workspace_size(int B, int H, int Hkv, int Nq, int d);
 fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* q, void* o, float* lse, const fa_strides* strides,

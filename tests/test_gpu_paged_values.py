@@ -51,3 +51,22 @@ def test_values_behind_scales_of_zero(B, Hkv, g, Nq, d, zeros):
                 c.t["v_scale"][pid, :, slot] = small
             compare(c, randn((B, Hkv * g, Nq, d), 423, 2.0))
             compare(c, randn((B, Hkv * g, Nq, d), 424, 2.0), window=160)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [1e-44, 1e-30, 1e-13, 2e38])
+def test_rows_of_zeros_under_any_scale(kind, scale):
+    """Rows without a score of their own: the mean of the values that the mask leaves."""
+    for B, Hkv, g, Nq, d in SHAPES[:5]:
+        lens = [20 + 11 * b for b in range(B - 1)] + [700]
+        c = Cache(lens, Hkv, d, 16, kind, "nhd", seed=451).fill_random(452)
+        q = torch.zeros((B, Hkv * g, Nq, d), dtype=torch.bfloat16)
+        compare(c, q, scale=scale)
+        compare(c, q, causal=False, window=9, scale=scale)
+        if scale < 1:
+            q[..., 1] = 2.0 ** -110
+            compare(c, q, window=9, scale=scale)
+        else:                                                  # keys of zeros, queries of any size
+            c.t["k_pages"].zero_()
+            q[..., 2:] = 2.0 ** 100
+            compare(c, q, window=9, scale=scale)

@@ -105,6 +105,12 @@ def test_attend_refusals(L):
     assert attend(L, c, H=2, Nq=(1 << 31) - 1) == INVALID
 
 
+def test_scales_out_of_range_are_refused(L):
+    for scale in (-1.0, float("inf"), 2.4e38, 3.4e38):                      # the kernels work with scale * log2(e)
+        assert attend(L, cache(), scale=scale) == INVALID
+        assert attend(L, cache(dtype=1), scale=scale) == INVALID
+
+
 def test_workspace_size(L):
     assert L.fa_fwd_paged_workspace_size(3, 4, 2, 1, 64) > 0
     for bad in ((0, 4, 2, 1, 64), (3, 5, 2, 1, 64), (3, 4, 2, 0, 64), (3, 4, 2, 1, 96)):
