@@ -182,6 +182,17 @@ __device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, volat
 __device__ __forceinline__ float paged_weight(float m, float l, float mt) {
   return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - mt);
 }
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+  return x;
+}
+// The smaller magnitude of two f16 pairs, each half by itself.
+__device__ __forceinline__ uint32_t min_abs_f16x2(uint32_t x, uint32_t y) {
+  uint32_t z;
+  asm("{\n .reg .b32 a;\n abs.f16x2 a, %1;\n min.f16x2 %0, a, %2;\n}" : "=r"(z) : "r"(x), "r"(y));
+  return z;
+}
 // Four e4m3 codes (the lowest first) as f16 numbers (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t* lo, uint32_t* hi) {
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
@@ -215,6 +226,78 @@ __device__ __forceinline__ int paged_slot(const PagedParams& p, int padded) {  /
 // a / b for a >= 0, b > 0: in 32 bits where they do, a fraction of the 64-bit division's instructions.
 __device__ __forceinline__ long long paged_div(long long a, long long b) {
   return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// Adds what rounding to f16 took from products below 2^-14 of 16 keys.  In parts: a row's rests down to 2^-28 of its
+// largest, scaled by a power of two that puts that one into [2^14, 2^15), then those that are left (those below 2^-111
+// share the last part).  A function of its own, whose accumulators pass through memory: inside the loop it costs every
+// path registers (128 ragged quantised sequences 106 us against 101 us).
+template <int D, int NB>
+struct PagedRests {
+  float acc[NB][D / 16][4], p[NB][4];  // as in the kernel; the products
+  uint32_t rows[4];  // this lane's D / 8 codes of keys 2 qd, + 1, + 8, + 9
+};
+template <int D, int NB>
+__device__ __noinline__ void paged_add_rests(PagedRests<D, NB>& t, uint32_t at) {
+  float r[NB][4];
+  bool left = false;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = t.p[nb][e];
+      r[nb][e] = fabsf(x) < 0x1p-14f ? x - __half2float(__float2half_rn(x)) : 0.f;
+      left |= r[nb][e] != 0.f;
+    }
+  while (__any_sync(0xffffffffu, left)) {
+    left = false;
+    uint32_t pp[NB][2];
+    float back[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float part[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t mx = max(__float_as_uint(r[nb][c]) & 0x7fffffffu, __float_as_uint(r[nb][2 + c]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const uint32_t e = max(mx >> 23, 15u);
+        const float up = __uint_as_float((268u - e) << 23);
+        back[nb][c] = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float& x = r[nb][2 * h + c];
+          const float y = x * up;
+          const bool now = !(fabsf(y) < 0x1p-14f) || e == 15u;
+          part[2 * h + c] = now ? y : 0.f;
+          x = now ? 0.f : x;
+          left |= x != 0.f;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pp[nb][h] = transpose8x8(pack_f16(part[2 * h], part[2 * h + 1]));
+    }
+#pragma unroll
+    for (int x = 0; x < D / 16; x += 2) {  // columns 2x, 2x + 1; 2x + 2, 2x + 3 of the lane's D / 8
+      uint32_t w[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) w[y] = ld_shared_u32(t.rows[y] + at + 2 * x);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t sel = z ? 0x7362 : 0x5140;
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_f16(__byte_perm(w[0], w[1], sel), &a0, &a1);
+        e4m3x4_to_f16(__byte_perm(w[2], w[3], sel), &a2, &a3);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16<true>(y, a0, a1, a2, a3, pp[nb]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t.acc[nb][x + z][i] = fmaf(y[i], back[nb][i & 1], t.acc[nb][x + z][i]);
+        }
+      }
+    }
+  }
 }
 
 struct PagedDesc {  // a tile, as the loading warp describes it to the others
@@ -504,9 +587,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
   const int hg = warp / (RG * KW), rg = warp / KW % RG, kw = warp % KW, qd = lane & 3, rq = lane >> 2;
   uint32_t qb[NB][QS][2];  // Q^T: row rq of each block, the k index in the order of the K fragments
   float acc[NB][DT][4];    // O^T: columns dcol(x, 0), dcol(x, 1) of V for rows 2 qd, 2 qd + 1
-  float mneg[NB][2], lim[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2], vtop = 0.f, vlow = 0.f;
+  float mneg[NB][2], lim[NB][2], l[NB][2], rowf[NB][2], vref[NB][2], vinv[NB][2], vtop = 0.f;
   int rlo[NB][2], rhi[NB][2];  // padded positions that the thread's rows may see
   int free_lo = 0, free_hi = 0;  // those that every row of the unit may see
+  bool settled = false;          // quantised: every row's accumulator has something large
   bool seg_starts_unit = false, fresh = true;  // fresh: the next tile begins a segment
   auto dcol = [&](int x, int e) { return kQuant ? rq * (D / 8) + 2 * x + e : 16 * x + 8 * e + rq; };
   // the queries of a unit, as they are in memory: words (8 s + qd, + 4) of a row, or its words 8 s + 2 qd, + 1 where
@@ -617,7 +701,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
         for (int x = 0; x < DT; ++x) acc[nb][x][0] = acc[nb][x][1] = acc[nb][x][2] = acc[nb][x][3] = 0.f;
       }
-      vtop = vlow = 0.f;
+      vtop = 0.f;
+      settled = false;
       free_lo = p.window < 0 ? 0 : paged_pad(p, max(0, L - 1 - p.window));
       free_hi = 0;
       if (L >= p.Nq)
@@ -705,12 +790,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         }
         auto on = [&](int k, int nb, int e) { return !edge || ((allowed >> (4 * (k * NB + nb) + e)) & 1) != 0; };
         // ---- running maximum: moved only when it grows by more than 8 (weights
-        // stay below 2^8).  Quantised: weights reach the second product as f16
-        // multiples of the largest value scale so far (vref, a power of two above
-        // it); a row's accumulator counts in units of its vref.  vtop and vlow
-        // bound the scales that leave all of a thread's rows as they are; a row
-        // that has seen scales of zero alone has no vref yet, and any other scale
-        // gives it one.
+        // stay below 2^8).  Quantised: a key reaches the second product as f16(weight
+        // * value scale / vref), and a row's accumulator counts in units of its vref,
+        // a power of two 2^7 below (the power of two above) the largest value scale
+        // so far: products stay below 2^15, and those of a key with that scale are
+        // normal numbers of f16 down to weights of 2^-20.  Scales below vtop leave all
+        // of a thread's rows as they are; a row that has seen scales of zero alone has
+        // no vref yet (vinv = 0), and any other scale gives it one.
         float arg[KS][NB][4];  // exponents: score - maximum, or the score itself before a row's first key (lim = -infinity)
         bool grow = false;
 #pragma unroll
@@ -731,8 +817,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
           for (int k = 0; k < KS; ++k) grow |= fmaxf(fabsf(vs[k][0]), fabsf(vs[k][1])) >= vtop;
         if (__any_sync(0xffffffffu, grow)) {
-          vtop = 0x1p127f;
-          vlow = 0.f;
+          vtop = INFINITY;
+          settled = false;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -761,17 +847,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
               l[nb][c] *= f;
               if (kQuant) {
                 if (vb != 0) {
-                  const float vn = fmaxf(vref[nb][c], __uint_as_float(min(max(vb >> 23, 1u) + 1u, 253u) << 23));
+                  const float vn = fmaxf(vref[nb][c], __uint_as_float(max(vb >> 23, 7u) - 6u << 23));
                   vinv[nb][c] = __uint_as_float((254u << 23) - __float_as_uint(vn));
                   f *= vref[nb][c] * vinv[nb][c];
                   vref[nb][c] = vn;
                 }
-                if (vref[nb][c] > 0x1p-126f) {
-                  vtop = fminf(vtop, vref[nb][c]);
-                  vlow = fmaxf(vlow, vref[nb][c] * 0x1p-12f);
-                } else if (lim[nb][c] > 0.f) {
+                if (vinv[nb][c] > 0.f)
+                  vtop = fminf(vtop, vref[nb][c] * 0x1p7f);
+                else if (lim[nb][c] > 0.f)
                   vtop = 0x1p-149f;
-                }
               }
 #pragma unroll
               for (int x = 0; x < DT; ++x) {
@@ -785,17 +869,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
             }
         }
         // The weights are rounded to 16 bits for the second product: bf16 (half a
-        // step is 2^-8 of a weight), or f16 of weight * value scale / vref, 2^-11
-        // of it down to 2^-14; keys whose scale is below 2^-12 vref take the slow
-        // form below.
+        // step is 2^-8 of a weight), or f16 of the product above, 2^-11 of it down to
+        // 2^-14.  Products below that (`low`) may be all that counts, beside a key of
+        // more weight whose value is zero: see behind the second product.
         uint32_t pb[KS][NB][2];
-        bool slow[KS];
+        bool low = false;
+        uint32_t least = 0x7bff7bffu;  // f16 pairs; a step without masks looks at what was rounded (zeros count as low)
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          slow[k] = false;
-          if (kQuant)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) slow[k] |= fabsf(vs[k][h]) < vlow && fabsf(vs[k][h]) > 0x1p-90f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -803,18 +884,25 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
               const float w = exp2_fast(arg[k][nb][e]);
               l[nb][e & 1] += w;
               sc[k][nb][e] = w;
-              if (kQuant) sc[k][nb][e] = on(k, nb, e) ? w * (vs[k][e >> 1] * vinv[nb][e & 1]) : 0.f;
+              if (kQuant) {
+                sc[k][nb][e] = on(k, nb, e) ? w * (vs[k][e >> 1] * vinv[nb][e & 1]) : 0.f;
+                if (edge) low |= fabsf(sc[k][nb][e]) < 0x1p-14f && sc[k][nb][e] != 0.f;
+              }
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              pb[k][nb][h] = transpose8x8(kQuant ? pack_f16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1])
-                                                 : pack_bf16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1]));
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t x = kQuant ? pack_f16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1])
+                                        : pack_bf16(sc[k][nb][2 * h], sc[k][nb][2 * h + 1]);
+              if (kQuant && !edge) least = min_abs_f16x2(x, least);
+              pb[k][nb][h] = transpose8x8(x);
+            }
           }
         }
+        if (kQuant && !edge) low = ((least - 0x04000400u) & 0x80008000u) != 0;
         // The slow form of columns dcol(x0 .. x0 + 3, .): products one by one in
         // fp32, weights of zero left out.  For an infinity or NaN among the values
         // of a tile that some rows see only in part (0 * infinity would reach rows
-        // that may not see that key), and for value scales too far apart for f16.
+        // that may not see that key).
         auto one_by_one = [&](int k, int x0) {
 #pragma unroll 1
           for (int y = 0; y < 16; ++y)
@@ -863,19 +951,21 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
                 for (int z = 0; z < D / 32; ++z) bad |= (w[y][z] & 0x7f7f7f7fu) + 0x01010101u;
               bad &= 0x80808080u;  // a NaN's code
             }
-            if (!__any_sync(0xffffffffu, slow[k] || bad)) {
-#pragma unroll
-              for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
-                const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16(__byte_perm(w[0][x >> 1], w[1][x >> 1], sel), &a0, &a1);
-                e4m3x4_to_f16(__byte_perm(w[2][x >> 1], w[3][x >> 1], sel), &a2, &a3);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[k][nb]);
-              }
-            } else {
+            if (edge && __any_sync(0xffffffffu, bad)) {
 #pragma unroll
               for (int x0 = 0; x0 < DT; x0 += 4) one_by_one(k, x0);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) sc[k][nb][0] = sc[k][nb][1] = sc[k][nb][2] = sc[k][nb][3] = 0.f;  // no rest
+              continue;
+            }
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {  // columns 2x, 2x + 1 of the thread's D / 8
+              const uint32_t sel = (x & 1) ? 0x7362 : 0x5140;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(__byte_perm(w[0][x >> 1], w[1][x >> 1], sel), &a0, &a1);
+              e4m3x4_to_f16(__byte_perm(w[2][x >> 1], w[3][x >> 1], sel), &a2, &a3);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16<true>(acc[nb][x], a0, a1, a2, a3, pb[k][nb]);
             }
           } else {
             const uint32_t from = vaddr + at[k];
@@ -900,6 +990,55 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) mma16<false>(acc[nb][x0 + x], a[x][0], a[x][1], a[x][2], a[x][3], pb[k][nb]);
             }
+          }
+        }
+        // What rounding takes from low products is at most 2^-25 of each: it does not matter beside a row's accumulator that
+        // has 2^10 in some column (2^15 keys: below 2^-11 of that).  Rows that have less get it added.
+        if constexpr (kQuant) {
+          if (!settled && __any_sync(0xffffffffu, low)) {
+            bool large = true;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float mx = rhi[nb][c] == 0 ? INFINITY : 0.f;  // rows that see nothing do not matter
+#pragma unroll
+                for (int x = 0; x < DT; ++x) mx = fmaxf(mx, fmaxf(fabsf(acc[nb][x][c]), fabsf(acc[nb][x][2 + c])));
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                large &= mx >= 0x1p10f;
+              }
+            settled = __all_sync(0xffffffffu, large);
+          }
+          if (!settled && __any_sync(0xffffffffu, low)) {
+            PagedRests<D, NB> t;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) t.rows[y] = smem_u32(pV + v_at(2 * qd + (y & 1) + 8 * (y >> 1), rq * (D / 8)));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int x = 0; x < DT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t.acc[nb][x][e] = acc[nb][x][e];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              // (the scales are loaded again: kept in registers they cost four rows a head 2%; the smallest that a write
+              // gives belongs to rows of zeros)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float v = __uint_as_float(ld_shared_u32(smem_u32(scl + HG * TK + (kb + 16 * k + 8 * (e >> 1)) * scl_step)));
+                  t.p[nb][e] = fabsf(v) > kAmaxLo / kE4m3Max ? sc[k][nb][e] : 0.f;
+                }
+              paged_add_rests<D, NB>(t, at[k]);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int x = 0; x < DT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nb][x][e] = t.acc[nb][x][e];
           }
         }
       }

@@ -43,7 +43,7 @@ SHAPES = [(2, 1, 1, 1, 128), (16, 4, 1, 1, 128), (16, 4, 2, 1, 64), (2, 4, 1, 1,
 def test_values_behind_scales_of_zero(B, Hkv, g, Nq, d, zeros):
     """A sequence begins with tokens whose value scale is zero (a placeholder, or
     another writer's rows of zeros) or subnormal; the tokens behind count in full."""
-    for small in (0.0, 2.0 ** -140):
+    for small in (0.0, 2.0 ** -140) if zeros == 64 else (0.0,):
         for lens in ([170 + 9 * b for b in range(B - 1)] + [2500], [zeros + 1 + b % 60 for b in range(B)]):
             c = Cache(lens, Hkv, d, 16, "e4m3", "nhd", seed=421).fill_random(422)
             for b in range(B):
@@ -51,6 +51,47 @@ def test_values_behind_scales_of_zero(B, Hkv, g, Nq, d, zeros):
                 c.t["v_scale"][pid, :, slot] = small
             compare(c, randn((B, Hkv * g, Nq, d), 423, 2.0))
             compare(c, randn((B, Hkv * g, Nq, d), 424, 2.0), window=160)
+
+
+@pytest.mark.parametrize("B,Hkv,g,Nq,d", SHAPES)
+@pytest.mark.parametrize("above", [7, 14, 21])
+def test_a_key_of_most_weight_without_a_value(B, Hkv, g, Nq, d, above):
+    """One key's score is far above all others' and its value row is zero, with a
+    scale of 2^10 or the smallest: the others make up the output."""
+    n = 800
+    for vscale in (None, 2.0 ** 10):
+        c = Cache([n] * B, Hkv, d, 64, "e4m3", "nhd", seed=431).fill_random(432)
+        q = randn((B, Hkv * g, Nq, d), 433)
+        q[..., 0] = 8.0
+        for b in range(B):
+            at = torch.tensor([(37 * b) % 70])
+            k = torch.zeros((1, Hkv, d), dtype=torch.bfloat16)
+            k[..., 0] = (math.log(n) + above) * math.sqrt(d) / 8.0
+            c.put("k", b, at, k)
+            c.put("v", b, at, torch.zeros((1, Hkv, d), dtype=torch.bfloat16))
+            if vscale is not None:
+                pid, slot = c.places(b, at)
+                c.t["v_scale"][pid, :, slot] = vscale
+        compare(c, q)
+
+
+@pytest.mark.parametrize("B,Hkv,g,Nq,d", SHAPES)
+def test_weights_far_apart(B, Hkv, g, Nq, d):
+    """Scores spread over a hundred and more, values larger the smaller their weight."""
+    lens = [90 + 7 * b for b in range(B)]
+    c = Cache(lens, Hkv, d, 16, "e4m3", "nhd", seed=441).fill_random(442)
+    q = randn((B, Hkv * g, Nq, d), 443)
+    q[..., 0] = 8.0
+    for b, n in enumerate(lens):
+        for j in range(n):
+            s = (j * 29) % 97                                  # the score, about
+            k = randn((1, Hkv, d), 444 + j, 0.1)
+            k[..., 0] = s * math.sqrt(d) / 8.0
+            c.put("k", b, torch.tensor([j]), k)
+            c.put("v", b, torch.tensor([j]), randn((1, Hkv, d), 644 + j, 2.0 ** min(127, 100 - s)) if s % 3 else
+                  torch.zeros((1, Hkv, d), dtype=torch.bfloat16))
+    compare(c, q)
+    compare(c, q, window=20)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
