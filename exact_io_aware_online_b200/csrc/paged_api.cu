@@ -280,7 +280,9 @@ fa_status launch_paged_rows(const fa_paged_cache* cache, const fa::PagedParams& 
   const int heads = paged_heads(p.c.B, p.R, p.c.Hkv, kQuant ? D : 2 * D);
   switch (paged_rows(p.R)) {
     case 8:
-      return heads == 4 ? launch_paged<D, kQuant, 1, 1, 4>(cache, p, st) : launch_paged<D, kQuant, 1, 1, 1>(cache, p, st);
+      if constexpr (kQuant || D == 64)  // rows of less than 256 bytes
+        if (heads == 4) return launch_paged<D, kQuant, 1, 1, 4>(cache, p, st);
+      return launch_paged<D, kQuant, 1, 1, 1>(cache, p, st);
     case 16:
       return heads == 2 ? launch_paged<D, kQuant, 1, 2, 2>(cache, p, st) : launch_paged<D, kQuant, 1, 2, 1>(cache, p, st);
     case 32: return launch_paged<D, kQuant, 1, 4, 1>(cache, p, st);

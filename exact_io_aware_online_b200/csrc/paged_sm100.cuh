@@ -18,7 +18,7 @@
 // kernel from 16 rows on.
 //
 // Work: the keys that some row of a unit (sequence, 1 to 4 kv heads, block of
-// rows) may see are cut into tiles of 16 to 128, about 32 KB.  The CTAs form
+// rows) may see are cut into tiles of 32 to 128, about 32 KB.  The CTAs form
 // groups of `lanes`, a lane for each unit of a sequence (or every lanes-th), so
 // that a group reads the same tokens' heads at the same time: heads inside
 // tokens are then whole DRAM rows, the 32-byte sectors of the scales are read
@@ -108,6 +108,7 @@ struct PagedCfg {
   static constexpr int kStatBytes = KW > 1 ? kPagedWarps * 8 * NB * 16 : 0;
   static constexpr int kSmemBytes = kStages * (kStageBytes + 16 + 48) + kStatBytes + 16 + 128;
   static_assert(kStages >= 2, "a tile loads while another is computed");
+  static_assert(kTile >= 32, "a warp's lanes load the scales of 32 keys");
   static_assert(2 * kScaleBytes <= 1024, "both tiles' scales fit behind the values");
   static_assert(KW == 1 || (HG == 1 && kPagedWarps * 8 * kMergeStride * 4 <= kStageBytes),
                 "the warps' accumulators are joined in a stage");
@@ -540,37 +541,34 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
       if (kQuant) {
         const long long at = on ? p.c.scales.row(cur.page, kh, cur.slot) : -1;
         const uint32_t to = smem_u32(dst + 2 * C::kTileBytes);
-        constexpr int TL = TK < 32 ? 32 : TK;  // a head's entries, in groups of 32
-        long long off[TL / 32];
-        bool here[TL / 32];
+        long long off[TK / 32];  // a head's entries, in groups of 32
+        bool here[TK / 32];
 #pragma unroll
-        for (int i = 0; i < TL / 32; ++i) {
+        for (int i = 0; i < TK / 32; ++i) {
           const int src = (i * 32 + lane) >> p.box_log, in = lane & (box - 1);
           off[i] = __shfl_sync(0xffffffffu, at, src);
           const int slot = __shfl_sync(0xffffffffu, cur.slot, src) + in;
           here[i] = off[i] >= 0 && slot < p.c.page_size;
           off[i] += in * p.c.scales.n;
         }
-        if (TK >= 32 || lane < TK) {
-          if (p.scale_rows) {  // [keys][heads]: the unit's heads in one copy
+        if (p.scale_rows) {  // [keys][heads]: the unit's heads in one copy
 #pragma unroll
-            for (int i = 0; i < TL / 32; ++i) {
-              const uint32_t at = to + (i * 32 + lane) * HG * 4;
-              const long long from = here[i] ? off[i] : 0;
-              cp_async<HG * 4>(at, p.c.ks + from, here[i]);
-              cp_async<HG * 4>(at + C::kScaleBytes, p.c.vs + from, here[i]);
-            }
-          } else {  // [heads][keys]
-#pragma unroll
-            for (int h = 0; h < HG; ++h)
-#pragma unroll
-              for (int i = 0; i < TL / 32; ++i) {
-                const uint32_t at = to + (h * TK + i * 32 + lane) * 4;
-                const long long from = here[i] ? off[i] + h * p.c.scales.h : 0;
-                cp_async<4>(at, p.c.ks + from, here[i]);
-                cp_async<4>(at + C::kScaleBytes, p.c.vs + from, here[i]);
-              }
+          for (int i = 0; i < TK / 32; ++i) {
+            const uint32_t at = to + (i * 32 + lane) * HG * 4;
+            const long long from = here[i] ? off[i] : 0;
+            cp_async<HG * 4>(at, p.c.ks + from, here[i]);
+            cp_async<HG * 4>(at + C::kScaleBytes, p.c.vs + from, here[i]);
           }
+        } else {  // [heads][keys]
+#pragma unroll
+          for (int h = 0; h < HG; ++h)
+#pragma unroll
+            for (int i = 0; i < TK / 32; ++i) {
+              const uint32_t at = to + (h * TK + i * 32 + lane) * 4;
+              const long long from = here[i] ? off[i] + h * p.c.scales.h : 0;
+              cp_async<4>(at, p.c.ks + from, here[i]);
+              cp_async<4>(at + C::kScaleBytes, p.c.vs + from, here[i]);
+            }
         }
         cp_async_arrive(full + st);
       }
@@ -660,7 +658,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<D, kQuant, NB, RG, HG>
         float back = p.scale_log2;  // what a product of the scaled queries is multiplied by
         if (kQuant) {
           // bf16 queries as f16: scaled by a power of two that puts the row's
-          // largest into [2^14, 2^15); exact down to 2^-32 of it
+          // largest into [2^14, 2^15); exact down to 2^-31 of it
           uint32_t mx = 0;
 #pragma unroll
           for (int s = 0; s < QS; ++s)
