@@ -27,6 +27,7 @@ HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "fa.h")
 
 FA_BF16, FA_FP32 = 0, 1
 FA_CACHE_BF16, FA_CACHE_E4M3 = 0, 1
+_INT_MAX = 2 ** 31 - 1  # ctypes takes wider numbers modulo 2^32
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_MISALIGNED",
           4: "FA_ERR_WORKSPACE", 5: "FA_ERR_CUDA", 6: "FA_ERR_TIMEOUT"}
 
@@ -754,7 +755,8 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
         if workspace is None else workspace
     code = _on(device, lib().fa_fwd_paged, c, q.data_ptr(), o.data_ptr(), l.data_ptr(),
                None if st is None else ctypes.addressof(st), H, Nq, 1.0 / math.sqrt(d) if scale is None else float(scale),
-               int(bool(causal)), int(window), ws.data_ptr(), ws.numel(), FA_BF16, _stream_ptr(device))
+               int(bool(causal)), max(-2, min(int(window), _INT_MAX)), ws.data_ptr(), ws.numel(), FA_BF16,
+               _stream_ptr(device))
     _check(code, "fa_fwd_paged")
     return o, l
 

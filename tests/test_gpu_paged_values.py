@@ -111,3 +111,17 @@ def test_rows_of_zeros_under_any_scale(kind, scale):
             c.t["k_pages"].zero_()
             q[..., 2:] = 2.0 ** 100
             compare(c, q, window=9, scale=scale)
+
+
+def test_windows_wider_than_any_cache():
+    """Half-widths beyond 32 bits are wide windows, not their low 32 bits; numbers below -1 are refused."""
+    c = Cache([90, 300], 2, 64, 16, "bf16", "nhd", seed=471).fill_random(472)
+    args, _ = c.cuda()
+    L, q = c.seqlens.cuda(), randn((2, 4, 1, 64), 473).cuda()
+    want = fa.fwd_paged(q, *args, L, causal=True)
+    for window in (300, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 10 ** 12, 2 ** 64):
+        o, lse = fa.fwd_paged(q, *args, L, causal=True, window=window)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), window
+    for window in (-2, -2 ** 31, -2 ** 32 - 1, -2 ** 64):
+        with pytest.raises(fa.FAError):
+            fa.fwd_paged(q, *args, L, causal=True, window=window)
