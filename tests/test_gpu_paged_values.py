@@ -113,6 +113,37 @@ def test_rows_of_zeros_under_any_scale(kind, scale):
             compare(c, q, window=9, scale=scale)
 
 
+def test_codes_and_values_of_extreme_rows():
+    """Every code, scale and value read back is the definition's in fp32, NaN where it is NaN."""
+    top = torch.finfo(torch.bfloat16).max
+    x = {"k": randn((10, 2, 64), 461), "v": randn((10, 2, 64), 462)}
+    for t in x.values():
+        t[0] = 0
+        t[1] = 2.0 ** -130                                     # below the clamp, subnormal in bf16
+        t[2] = top
+        t[3, 0, 7] = math.inf
+        t[4, 1, 8] = -math.inf
+        t[5, 0, 9] = math.nan
+        t[6] *= 2.0 ** -99
+        t[7, 0, 1:] = 0
+        t[8, 0, 0], t[8, 0, 1] = math.nan, math.inf
+        t[9, :, :32], t[9, :, 32:] = top, -2.0 ** 120
+    c = Cache([10], 2, 64, 4, "e4m3", seed=463)
+    (k, v, table), scales = c.cuda()
+    cu, L = torch.tensor([0, 10], dtype=torch.int32, device="cuda"), c.seqlens.cuda()
+    fa.cache_write(x["k"].cuda(), x["v"].cuda(), k, v, table, cu, L, **scales)
+    rk, rv = fa.cache_read(k, v, table, cu, L, 10, **scales)
+    pid, slot = c.places(0, torch.arange(10))
+    for name, pages, back in (("k", k, rk), ("v", v, rv)):
+        code, scale = quantise(x[name])
+        got = pages.cpu().view(torch.uint8)[pid, :, slot].view(torch.float8_e4m3fn).float()
+        torch.testing.assert_close(got, code.float(), rtol=0, atol=0, equal_nan=True)
+        torch.testing.assert_close(scales[name + "_scale"].cpu()[pid, :, slot], scale, rtol=0, atol=0, equal_nan=True)
+        want = (code.float() * scale[..., None]).to(torch.bfloat16)
+        torch.testing.assert_close(back.cpu(), want, rtol=0, atol=0, equal_nan=True)
+        assert int(torch.isnan(want).sum()) == 2 * 64 and torch.isinf(want).any()
+
+
 def test_windows_wider_than_any_cache():
     """Half-widths beyond 32 bits are wide windows, not their low 32 bits; numbers below -1 are refused."""
     c = Cache([90, 300], 2, 64, 16, "bf16", "nhd", seed=471).fill_random(472)
@@ -125,3 +156,11 @@ def test_windows_wider_than_any_cache():
     for window in (-2, -2 ** 31, -2 ** 32 - 1, -2 ** 64):
         with pytest.raises(fa.FAError):
             fa.fwd_paged(q, *args, L, causal=True, window=window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_chunk_of_a_prompt(kind):
+    """Hundreds of new tokens over a cache: many blocks of rows, more units of a sequence than CTAs."""
+    c = Cache([700, 130, 0], 8, 64, 16, kind, "nhd", seed=481).fill_random(482)
+    compare(c, randn((3, 16, 260, 64), 483, 2.0))
+    compare(c, randn((3, 16, 260, 64), 484, 2.0), window=40)
