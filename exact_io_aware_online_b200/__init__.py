@@ -728,7 +728,8 @@ def fwd_paged(q, k_pages, v_pages, page_table, seqlens, k_scale=None, v_scale=No
     """O, LSE of each sequence's newest Nq tokens, q [B,H,Nq,d] (bfloat16, any
     layout with d contiguous), over a paged cache that holds their keys and
     values already: fwd_decode() for sequences of different lengths (see
-    fa_fwd_paged in fa.h; the cache's tensors are those of cache_write())."""
+    fa_fwd_paged in fa.h; the cache's tensors are those of cache_write()).  Made
+    for a few new tokens; for hundreds cache_read() and fwd_decode() are faster."""
     import torch
     c, device, B, Hkv, d = _cache_of(k_pages, v_pages, page_table, seqlens, k_scale, v_scale)
     shape = q.shape

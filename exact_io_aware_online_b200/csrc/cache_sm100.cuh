@@ -101,11 +101,11 @@ __device__ __forceinline__ int first_sequence(const int* cu, int B, int t, int l
 // stores fill sectors) and a warp 8 * kMoveUnroll rows, which may belong to
 // several tokens.  Few lanes a row keep what a row costs once -- the join of
 // the maximum, two divisions, addresses -- small beside its bytes (sixteen lanes
-// a row: writing 131072 quantised tokens 199 us against 127 us); a write loads
+// a row: writing 131072 quantised tokens 199 us against 127 us then); a write loads
 // its rows before it looks up where they go.  Bound by HBM from a few thousand
 // tokens on, by the launch and four dependent loads below.  Measured, of the
-// copy rate of 6561 GB/s: that write 127 us (97%), reading a ragged quantised batch back
-// 117 us (97%), 256 short bf16 sequences at d = 64 53 us (93%), one token each of 64
+// copy rate of 6561 GB/s: that write 129 us (96%), reading a ragged quantised batch back
+// 118 us (96%), 256 short bf16 sequences at d = 64 53 us (93%), one token each of 64
 // sequences 2.8 us (11 us a call with the host's side).
 constexpr int kMoveWarps = 4;
 constexpr int kMoveUnroll = 2;

@@ -315,7 +315,11 @@ fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_
  * without an allowed key, get O = 0, LSE = -inf; what masked tokens and unused
  * parts of pages hold has no effect.  Every key and value that some row may see
  * is read once for the H / Hkv query heads that share it, as long as their
- * (H / Hkv) * Nq rows are at most 64 (once per 64 rows otherwise).
+ * (H / Hkv) * Nq rows are at most 64.  More rows are taken 64 at a time, and
+ * each 64 walk the keys of all Nq rows, those that the mask takes from them
+ * included: the call is made for a few new tokens.  For hundreds (a prompt's
+ * chunk) fa_cache_read and fa_fwd_decode (sequences of one length) or
+ * fa_fwd_packed (whole prompts) are faster.
  * Any page_size goes; multiples of 16 load best (others are taken as the next
  * multiple of 8 tokens long: page_size rounded up so, times max_pages, is at
  * most 2^30, FA_ERR_UNSUPPORTED otherwise).
@@ -328,7 +332,11 @@ fa_status fa_cache_read(const fa_paged_cache* cache, void* k, void* v, const fa_
  * Deterministic; a sequence's last bits depend on the other lengths of the
  * batch.  Arithmetic: scores, maxima, sums and accumulators in fp32; the
  * weights enter the second product as bf16 (bf16 pages) or, times the value's
- * scale, as f16 (E4M3 pages).  dtype: FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
+ * scale, as f16 (E4M3 pages: what f16 cannot hold of small ones is added where
+ * it could be seen in O, but for values whose scale is the smallest that a
+ * write gives).  Queries of E4M3 pages enter the first product as f16, scaled
+ * row by row: exact down to 2^-31 of the row's largest component.  dtype:
+ * FA_BF16 (FA_ERR_UNSUPPORTED otherwise).
  * Other errors as fa_fwd; FA_ERR_INVALID_ARG also for a scale whose product
  * with log2(e) overflows fp32, FA_ERR_UNSUPPORTED also where the table could
  * hold more tiles than 32 bits count.
